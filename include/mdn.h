@@ -433,6 +433,185 @@ mdn_status mdn_chunk_fwd_noalloc(const void *q, const void *k, const void *v,
                                  int flags, mdn_stream_t stream);
 
 /*
+ * The gated delta rule
+ * --------------------
+ * The delta rule without momentum (mu = 0 in the recurrence at the top, which
+ * the functions above cannot express: mu_log = -inf has no finite
+ * differences), with one state per head.  Per value head, alpha =
+ * exp(alpha_log):
+ *
+ *     vtilde_t = v_t - alpha_t S_{t-1}^T k_t
+ *     S_t      = alpha_t S_{t-1} + beta_t k_t vtilde_t^T
+ *     o_t      = scale S_t^T q_t
+ *
+ * Conventions are those at the top, with these differences: q and k have Hk
+ * heads and v has H, a multiple of Hk; value head h uses key head
+ * h / (H / Hk).  The gates have H heads.  alpha_log and beta are taken as
+ * given (no clamp); scale is finite.  All states are fp32 and are held in
+ * fp32 for the whole sequence.  Support: d_k = d_v in {64, 128}, C = 64, fp32
+ * or bf16.
+ */
+
+/*
+ * Bytes of device scratch of the chunk calls below for these sizes and flags,
+ * or 0 if the sizes are invalid or unsupported.  Pure host functions.
+ */
+size_t mdn_gdr_chunk_fwd_workspace_size(int B, int T, int Hk, int H, int dk, int dv, int C,
+                                        mdn_dtype in_dtype, int flags);
+size_t mdn_gdr_chunk_fwd_varlen_workspace_size(int N, int total_T, int Hk, int H, int dk, int dv,
+                                               int C, mdn_dtype in_dtype, int flags);
+size_t mdn_gdr_chunk_bwd_workspace_size(int B, int T, int Hk, int H, int dk, int dv, int C,
+                                        mdn_dtype in_dtype, int flags);
+size_t mdn_gdr_chunk_bwd_varlen_workspace_size(int N, int total_T, int Hk, int H, int dk, int dv,
+                                               int C, mdn_dtype in_dtype, int flags);
+
+/*
+ * The pass over whole sequences.
+ *
+ *   q, k        [B,T,Hk,d], v [B,T,H,d] in_dtype; alpha_log, beta [B,T,H] fp32.
+ *   S0          [B,H,d,d] fp32 entering states or NULL (zeros).
+ *   o           [B,T,H,d] in_dtype.  vtilde  the same, or NULL (not written;
+ *               mdn_gdr_chunk_bwd needs it).
+ *   S_T         [B,H,d,d] fp32; may be S0.
+ *   workspace   at least the size above for the same flags, 256-byte aligned.
+ *               Calls that may overlap need workspaces of their own.
+ *   flags       MDN_CHECK_FINITE and/or MDN_FORCE_SIMT.
+ *
+ * Any T >= 0 (T = 0 copies S0 to S_T).  Pointers to q, k, v, o, vtilde and the
+ * states are 16-byte aligned.  Asynchronous on `stream` (except with
+ * MDN_CHECK_FINITE); can be captured in a CUDA graph.  The workspace's status
+ * words can be read with mdn_chunk_fwd_status.  Errors as mdn_chunk_fwd.
+ */
+mdn_status mdn_gdr_chunk_fwd(const void *q, const void *k, const void *v, mdn_dtype in_dtype,
+                             const float *alpha_log, const float *beta, float scale,
+                             const float *S0, int B, int T, int Hk, int H, int dk, int dv, int C,
+                             void *o, void *vtilde, float *S_T, void *workspace, size_t ws_bytes,
+                             int flags, mdn_stream_t stream);
+
+/*
+ * The same over N sequences packed along the token axis.
+ *
+ *   q, k        [total_T,Hk,d], v, o, vtilde [total_T,H,d]; gates [total_T,H].
+ *   cu_seqlens  DEVICE pointer to N+1 ints, read on the device only:
+ *               cu_seqlens[0] = 0, non-decreasing, cu_seqlens[N] <= total_T.
+ *               Rows of o and vtilde behind cu_seqlens[N] are left as they
+ *               were, and those of the inputs are not read into any result.
+ *               Sequences may be empty (their S_T is S0).
+ *   S0, S_T     [N,H,d,d].
+ *
+ * Offsets that break these rules make every sequence empty; MDN_CHECK_FINITE
+ * or mdn_chunk_fwd_status then report MDN_ERR_INVALID_ARG.  With
+ * MDN_CHECK_FINITE only S_T is scanned.
+ */
+mdn_status mdn_gdr_chunk_fwd_varlen(const void *q, const void *k, const void *v,
+                                    mdn_dtype in_dtype, const float *alpha_log, const float *beta,
+                                    float scale, const int *cu_seqlens, int N, int total_T,
+                                    const float *S0, int Hk, int H, int dk, int dv, int C, void *o,
+                                    void *vtilde, float *S_T, void *workspace, size_t ws_bytes,
+                                    int flags, mdn_stream_t stream);
+
+/*
+ * Gradients of L = <d_o, o> + <dS_T, S_T>, from the vtilde that the forward
+ * pass saved (v itself is not needed): the states are rebuilt from vtilde as
+ * it was stored, and with G_t the adjoint of S_t
+ *
+ *     dv_t = beta_t G_t^T k_t              dq_t = scale S_t d_o_t
+ *     dk_t = beta_t G_t vtilde_t - alpha_t S_{t-1} dv_t
+ *     dbeta_t = k_t^T G_t vtilde_t         dalpha_log_t = alpha_t <G_t - k_t dv_t^T, S_{t-1}>
+ *
+ *   dS_T        [B,H,d,d] fp32 or NULL (zero).
+ *   dq, dk      [B,T,Hk,d] in_dtype, summed over the value heads of a key head.
+ *   dv_out      [B,T,H,d] in_dtype.
+ *   dalpha_log, dbeta  [B,T,H] fp32;  dS0  [B,H,d,d] fp32 (required).
+ *   flags       MDN_CHECK_FINITE and/or MDN_FORCE_SIMT.
+ * Everything else as mdn_gdr_chunk_fwd.
+ */
+mdn_status mdn_gdr_chunk_bwd(const void *q, const void *k, mdn_dtype in_dtype,
+                             const float *alpha_log, const float *beta, float scale,
+                             const float *S0, const void *vtilde, const void *d_o,
+                             const float *dS_T, int B, int T, int Hk, int H, int dk, int dv, int C,
+                             void *dq, void *dk_out, void *dv_out, float *dalpha_log, float *dbeta,
+                             float *dS0, void *workspace, size_t ws_bytes, int flags,
+                             mdn_stream_t stream);
+
+/* Gradients of mdn_gdr_chunk_fwd_varlen; shapes and cu_seqlens as there (rows
+ * of the outputs behind the last sequence are left as they were; with broken
+ * offsets dS0 is dS_T and nothing else is written). */
+mdn_status mdn_gdr_chunk_bwd_varlen(const void *q, const void *k, mdn_dtype in_dtype,
+                                    const float *alpha_log, const float *beta, float scale,
+                                    const int *cu_seqlens, int N, int total_T, const float *S0,
+                                    const void *vtilde, const void *d_o, const float *dS_T, int Hk,
+                                    int H, int dk, int dv, int C, void *dq, void *dk_out,
+                                    void *dv_out, float *dalpha_log, float *dbeta, float *dS0,
+                                    void *workspace, size_t ws_bytes, int flags,
+                                    mdn_stream_t stream);
+
+/*
+ * One decode token for every (b, h).
+ *
+ *   q, k        [B,Hk,d], v [B,H,d] in_dtype; alpha_log, beta [B,H] fp32.
+ *   S           [B,H,d,d] fp32, the state before the token; S_out the state
+ *               after it: S itself (in place), or a buffer that does not
+ *               overlap it (S is then kept, for a caller that may drop the token).
+ *   o           [B,H,d] in_dtype; vtilde the same or NULL.
+ *   flags       must be 0 (reserved).
+ * S and S_out 16-byte aligned, every other pointer aligned to its element
+ * type.  Each state element is read once and written once.
+ * Errors: MDN_ERR_INVALID_ARG, MDN_ERR_UNSUPPORTED, MDN_ERR_CUDA.
+ */
+mdn_status mdn_gdr_step(const void *q, const void *k, const void *v, mdn_dtype in_dtype,
+                        const float *alpha_log, const float *beta, float scale, const float *S,
+                        float *S_out, int B, int Hk, int H, int dk, int dv, void *o, void *vtilde,
+                        int flags, mdn_stream_t stream);
+
+/* Activations of mdn_group_norm_fwd / _bwd. */
+#define MDN_ACT_NONE 0
+#define MDN_ACT_SILU 1 /* z sigmoid(z) */
+
+/*
+ * Group norm with an activation, channels last: the norm that follows a token
+ * mixer.  x is [N, L, C] with C in G groups of C / G neighbouring channels; a
+ * group's statistics are over its L x C/G values of one n.  The mixers' output
+ * [B,T,H,d] normed token by token and head by head is N = B T, L = 1,
+ * C = H d, G = H; L = T norms whole sequences.
+ *
+ *     xhat = (x - mean) / sqrt(var + eps),  n = xhat weight + bias
+ *     y = act(n) without a gate,  y = n act(gate) with one
+ *
+ *   x, gate, y  [N,L,C] dtype; gate may be NULL.
+ *   weight, bias  [C] fp32, both or neither (NULL: 1 and 0).
+ *   eps         >= 0.  var is the mean squared distance from the mean.
+ *   mean, rstd  [N,G] fp32 outputs (the backward pass reads them).
+ *   workspace   at least mdn_group_norm_workspace_size(..., 0) bytes, 16-byte
+ *               aligned; NULL where that is 0 (L = 1 and up to 256 channels a
+ *               group at any alignment).
+ * Any sizes with C % G = 0 and N G < 2^30, C < 2^22; N <= 65535 unless L = 1 and
+ * C / G <= 256.  Pointers need the alignment of their element type (16-byte
+ * aligned tensors with groups of whole 16-byte pieces take a vectorised path).
+ * Outputs may not alias inputs.  Asynchronous on `stream`.
+ * Errors: MDN_ERR_INVALID_ARG, MDN_ERR_UNSUPPORTED, MDN_ERR_CUDA.
+ */
+size_t mdn_group_norm_workspace_size(int N, int L, int C, int G, mdn_dtype dtype, int backward);
+mdn_status mdn_group_norm_fwd(const void *x, const void *gate, mdn_dtype dtype, const float *weight,
+                              const float *bias, int N, int L, int C, int G, float eps, int act,
+                              void *y, float *mean, float *rstd, void *workspace, size_t ws_bytes,
+                              mdn_stream_t stream);
+
+/*
+ * Its gradients from the saved mean and rstd.
+ *
+ *   dy, dx, dgate  [N,L,C] dtype; dgate with a gate, else NULL.
+ *   dweight, dbias [C] fp32, both or neither; only with weight and bias.  The
+ *                  sums run in a fixed order: equal calls give equal bits.
+ *   workspace   at least mdn_group_norm_workspace_size(..., 1) bytes.
+ */
+mdn_status mdn_group_norm_bwd(const void *x, const void *gate, mdn_dtype dtype, const float *weight,
+                              const float *bias, const float *mean, const float *rstd,
+                              const void *dy, int N, int L, int C, int G, int act, void *dx,
+                              void *dgate, float *dweight, float *dbias, void *workspace,
+                              size_t ws_bytes, mdn_stream_t stream);
+
+/*
  * Optional per-kernel timing (no counterpart in the method; a measurement aid).
  * mdn_profile_enable(1) makes every later kernel launch of the library record a
  * CUDA event pair on its launch stream (the events are created on the first

@@ -18,6 +18,8 @@ MDN_SLICE128 = 0x10
 MDN_TEST_NO_INTRA = 0x100
 MDN_ETA_TANH = 0
 MDN_ETA_2SIGMOID = 1
+MDN_ACT_NONE = 0
+MDN_ACT_SILU = 1
 
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 
@@ -53,6 +55,24 @@ SIGNATURES = {
                                  _vp, _vp, _vp, _vp, _vp, _vp]),
     "mdn_chunk_fwd_noalloc": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _f, _vp, _vp,
                                    _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _vp]),
+    **{f"mdn_gdr_chunk_{n}_workspace_size": (_sz, [_i] * 9)
+       for n in ("fwd", "fwd_varlen", "bwd", "bwd_varlen")},
+    "mdn_gdr_chunk_fwd": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _f, _vp, _i, _i, _i, _i, _i, _i, _i,
+                               _vp, _vp, _vp, _vp, _sz, _i, _vp]),
+    "mdn_gdr_chunk_fwd_varlen": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _f, _vp, _i, _i, _vp, _i, _i,
+                                      _i, _i, _i, _vp, _vp, _vp, _vp, _sz, _i, _vp]),
+    "mdn_gdr_chunk_bwd": (_i, [_vp, _vp, _i, _vp, _vp, _f, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i,
+                               _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _i, _vp]),
+    "mdn_gdr_chunk_bwd_varlen": (_i, [_vp, _vp, _i, _vp, _vp, _f, _vp, _i, _i, _vp, _vp, _vp, _vp,
+                                      _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
+                                      _i, _vp]),
+    "mdn_gdr_step": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _f, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp,
+                          _i, _vp]),
+    "mdn_group_norm_workspace_size": (_sz, [_i] * 6),
+    "mdn_group_norm_fwd": (_i, [_vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp, _vp, _vp,
+                                _vp, _sz, _vp]),
+    "mdn_group_norm_bwd": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp,
+                                _vp, _vp, _vp, _vp, _sz, _vp]),
     "mdn_profile_enable": (_i, [_i]),
     "mdn_profile_read": (_i, [_i, ctypes.POINTER(ctypes.c_char_p),
                               ctypes.POINTER(ctypes.c_double),

@@ -1,0 +1,316 @@
+// The C entry points of the gated delta rule (include/mdn.h, mdn_gdr_*):
+// argument validation, workspace layout and kernel dispatch.
+#include <cmath>
+
+#include "gdr_internal.cuh"
+
+using namespace mdn;
+
+namespace {
+
+constexpr size_t kAlign = 256;
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool aligned_elem(const void* p, mdn_dtype dt)
+{
+    return (reinterpret_cast<uintptr_t>(p) & (dt == MDN_F32 ? 3u : 1u)) == 0;
+}
+
+// One call's sizes.  packed: B = sequences, T = tokens of the packed buffer.
+struct Sizes {
+    int B, T, Hk, H, dk, dv, C;
+    mdn_dtype dt;
+    bool packed;
+    long long rows() const { return packed ? T : (long long)B * T; }
+    // chunks of the call: every sequence ends in at most one partial chunk
+    long long chunks() const
+    {
+        return packed ? (long long)T / C + B : (long long)B * (((long long)T + C - 1) / C);
+    }
+};
+
+mdn_status check_sizes(const Sizes& z)
+{
+    if (z.B < 0 || z.T < 0 || z.H < 0 || z.Hk < 0 || z.dk <= 0 || z.dv <= 0 || z.C <= 0)
+        return MDN_ERR_INVALID_ARG;
+    if (z.H > 0 && (z.Hk == 0 || z.H % z.Hk != 0)) return MDN_ERR_INVALID_ARG;
+    if (z.dt != MDN_F32 && z.dt != MDN_BF16) return MDN_ERR_UNSUPPORTED;
+    if (z.dk != z.dv || (z.dk != 64 && z.dk != 128) || z.C != kChunk) return MDN_ERR_UNSUPPORTED;
+    // grids and 32-bit chunk indices
+    if (z.chunks() * z.H >= (1LL << 31) || (long long)z.B * z.H >= (1LL << 31) / 4 ||
+        z.chunks() * z.C >= (1LL << 31))
+        return MDN_ERR_UNSUPPORTED;
+    return MDN_OK;
+}
+
+struct Layout {
+    size_t status, cu_s, cu_c, seq_order, chunk_order;
+    size_t SS, GG, dvf, dqp, dkp;  // backward
+    size_t total;
+};
+
+Layout layout(const Sizes& z, bool bwd)
+{
+    Layout w = {};
+    size_t off = align_up(64);  // status words first: mdn_chunk_fwd_status reads them there
+    if (z.packed) {
+        w.cu_s = off;        off += align_up((size_t)(z.B + 1) * sizeof(int));
+        w.cu_c = off;        off += align_up((size_t)(z.B + 1) * sizeof(int));
+        w.seq_order = off;   off += align_up((size_t)z.B * sizeof(int));
+        w.chunk_order = off; off += align_up((size_t)z.chunks() * sizeof(int));
+    }
+    if (bwd) {
+        const size_t states = (size_t)z.chunks() * z.H * z.dk * z.dv * sizeof(float);
+        const size_t tok = (size_t)z.rows() * z.H * z.dk * sizeof(float);
+        w.SS = off;  off += align_up(states);
+        w.GG = off;  off += align_up(states);
+        w.dvf = off; off += align_up(tok);
+        if (z.H > z.Hk) {
+            w.dqp = off; off += align_up(tok);
+            w.dkp = off; off += align_up(tok);
+        }
+    }
+    w.total = off;
+    return w;
+}
+
+size_t ws_size(const Sizes& z, bool bwd)
+{
+    return check_sizes(z) == MDN_OK ? layout(z, bwd).total : 0;
+}
+
+// Clears the status words and, for packed sequences, checks the offsets.
+mdn_status begin(gdr::Args& a, const Sizes& z, const Layout& w, char* ws, const int* cu_seqlens,
+                 cudaStream_t s)
+{
+    a.B = z.B; a.T = z.T; a.Hk = z.Hk; a.H = z.H; a.D = z.dk;
+    a.NT = (int)(z.packed ? z.chunks() : ((long long)z.T + z.C - 1) / z.C);
+    a.status = reinterpret_cast<unsigned*>(ws + w.status);
+    cudaError_t e = cudaMemsetAsync(a.status, 0, 64, s);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (!z.packed) return MDN_OK;
+    int* cu_s = reinterpret_cast<int*>(ws + w.cu_s);
+    int* cu_c = reinterpret_cast<int*>(ws + w.cu_c);
+    int* seq = reinterpret_cast<int*>(ws + w.seq_order);
+    e = launch_varlen_setup(cu_seqlens, z.B, z.T, a.NT, cu_s, cu_c, seq,
+                            reinterpret_cast<int*>(ws + w.chunk_order), a.status + 2, s,
+                            /*exact=*/false);
+    if (e != cudaSuccess) return cuda_fail(e);
+    a.cu_s = cu_s; a.cu_c = cu_c; a.seq_order = seq;
+    return MDN_OK;
+}
+
+struct Out {
+    const void* p;
+    size_t n;
+    bool bf16;
+};
+
+// MDN_CHECK_FINITE: scan the outputs, synchronise and report.
+mdn_status report(const Out* outs, int n, unsigned* status, cudaStream_t s)
+{
+    cudaError_t e;
+    for (int i = 0; i < n; ++i)
+        if (outs[i].p && (e = launch_finite_check(outs[i].p, outs[i].n, outs[i].bf16, status, s)))
+            return cuda_fail(e);
+    unsigned host[3] = {0, 0, 0};
+    if ((e = cudaMemcpyAsync(host, status, sizeof(host), cudaMemcpyDeviceToHost, s))) return cuda_fail(e);
+    if ((e = cudaStreamSynchronize(s))) return cuda_fail(e);
+    if (host[2]) return MDN_ERR_INVALID_ARG;
+    if (host[1]) return MDN_ERR_TIMEOUT;
+    return host[0] ? MDN_ERR_NONFINITE : MDN_OK;
+}
+
+mdn_status fwd_impl(const Sizes& z, const void* q, const void* k, const void* v,
+                    const float* alpha_log, const float* beta, float scale, const int* cu_seqlens,
+                    const float* S0, void* o, void* vtilde, float* S_T, void* workspace,
+                    size_t ws_bytes, int flags, mdn_stream_t stream)
+{
+    mdn_status st = check_sizes(z);
+    if (st != MDN_OK) return st;
+    if (flags & ~(MDN_CHECK_FINITE | MDN_FORCE_SIMT)) return MDN_ERR_INVALID_ARG;
+    if (!std::isfinite(scale)) return MDN_ERR_INVALID_ARG;
+    if (z.B == 0 || z.H == 0) return MDN_OK;
+    if (z.packed && (!cu_seqlens || !aligned4(cu_seqlens))) return MDN_ERR_INVALID_ARG;
+    if (!S_T || !aligned16(S_T) || !aligned16(S0)) return MDN_ERR_INVALID_ARG;
+    if (z.rows() > 0) {
+        const void* tok[] = {q, k, v, o};
+        for (const void* p : tok)
+            if (!p || !aligned16(p)) return MDN_ERR_INVALID_ARG;
+        if (!aligned16(vtilde)) return MDN_ERR_INVALID_ARG;
+        if (!alpha_log || !beta || !aligned4(alpha_log) || !aligned4(beta)) return MDN_ERR_INVALID_ARG;
+    }
+    if (!workspace || reinterpret_cast<uintptr_t>(workspace) % kAlign) return MDN_ERR_INVALID_ARG;
+    const Layout w = layout(z, false);
+    if (ws_bytes < w.total) return MDN_ERR_INVALID_ARG;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    gdr::Args a;
+    a.q = q; a.k = k; a.v = v; a.alpha_log = alpha_log; a.beta = beta; a.scale = scale; a.S0 = S0;
+    a.o = o; a.vt = vtilde; a.S_T = S_T;
+    if ((st = begin(a, z, w, ws, cu_seqlens, s)) != MDN_OK) return st;
+    const cudaError_t e = gdr::launch_fwd_simt(a, z.dt, s);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (!(flags & MDN_CHECK_FINITE)) return MDN_OK;
+    const bool bf = z.dt == MDN_BF16;
+    const size_t tok = (size_t)z.rows() * z.H * z.dk, sta = (size_t)z.B * z.H * z.dk * z.dv;
+    // a packed buffer may have rows behind its last sequence, which the pass does not write
+    const Out outs[] = {{z.packed ? nullptr : o, tok, bf}, {z.packed ? nullptr : vtilde, tok, bf},
+                        {S_T, sta, false}};
+    return report(outs, 3, a.status, s);
+}
+
+mdn_status bwd_impl(const Sizes& z, const void* q, const void* k, const float* alpha_log,
+                    const float* beta, float scale, const int* cu_seqlens, const float* S0,
+                    const void* vtilde, const void* d_o, const float* dS_T, void* dq, void* dk_out,
+                    void* dv_out, float* dalpha_log, float* dbeta, float* dS0, void* workspace,
+                    size_t ws_bytes, int flags, mdn_stream_t stream)
+{
+    mdn_status st = check_sizes(z);
+    if (st != MDN_OK) return st;
+    if (flags & ~(MDN_CHECK_FINITE | MDN_FORCE_SIMT)) return MDN_ERR_INVALID_ARG;
+    if (!std::isfinite(scale)) return MDN_ERR_INVALID_ARG;
+    if (z.B == 0 || z.H == 0) return MDN_OK;
+    if (z.packed && (!cu_seqlens || !aligned4(cu_seqlens))) return MDN_ERR_INVALID_ARG;
+    if (!dS0 || !aligned16(dS0) || !aligned16(dS_T) || !aligned16(S0)) return MDN_ERR_INVALID_ARG;
+    if (z.rows() > 0) {
+        const void* tok[] = {q, k, vtilde, d_o, dq, dk_out, dv_out};
+        for (const void* p : tok)
+            if (!p || !aligned16(p)) return MDN_ERR_INVALID_ARG;
+        const void* g[] = {alpha_log, beta, dalpha_log, dbeta};
+        for (const void* p : g)
+            if (!p || !aligned4(p)) return MDN_ERR_INVALID_ARG;
+    }
+    if (!workspace || reinterpret_cast<uintptr_t>(workspace) % kAlign) return MDN_ERR_INVALID_ARG;
+    const Layout w = layout(z, true);
+    if (ws_bytes < w.total) return MDN_ERR_INVALID_ARG;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    gdr::Args a;
+    a.q = q; a.k = k; a.v = nullptr; a.alpha_log = alpha_log; a.beta = beta; a.scale = scale; a.S0 = S0;
+    a.o = nullptr; a.vt = const_cast<void*>(vtilde); a.S_T = nullptr;
+    a.d_o = d_o; a.dS_T = dS_T; a.dq = dq; a.dk = dk_out; a.dv = dv_out;
+    a.dalpha_log = dalpha_log; a.dbeta = dbeta; a.dS0 = dS0;
+    a.SS = reinterpret_cast<float*>(ws + w.SS);
+    a.GG = reinterpret_cast<float*>(ws + w.GG);
+    a.dvf = reinterpret_cast<float*>(ws + w.dvf);
+    a.dqp = w.dqp ? reinterpret_cast<float*>(ws + w.dqp) : nullptr;
+    a.dkp = w.dkp ? reinterpret_cast<float*>(ws + w.dkp) : nullptr;
+    if ((st = begin(a, z, w, ws, cu_seqlens, s)) != MDN_OK) return st;
+    cudaError_t e = gdr::launch_bwd_simt(a, z.dt, s);
+    if (e == cudaSuccess && a.dqp) e = gdr::launch_fold_heads(a, z.dt, s);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (!(flags & MDN_CHECK_FINITE)) return MDN_OK;
+    const bool bf = z.dt == MDN_BF16;
+    const size_t tok = (size_t)z.rows() * z.H, key = (size_t)z.rows() * z.Hk * z.dk;
+    const bool whole = !z.packed;  // as in the forward pass
+    const Out outs[] = {{whole ? dq : nullptr, key, bf}, {whole ? dk_out : nullptr, key, bf},
+                        {whole ? dv_out : nullptr, tok * z.dk, bf},
+                        {whole ? dalpha_log : nullptr, tok, false}, {whole ? dbeta : nullptr, tok, false},
+                        {dS0, (size_t)z.B * z.H * z.dk * z.dv, false}};
+    return report(outs, 6, a.status, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mdn_gdr_chunk_fwd_workspace_size(int B, int T, int Hk, int H, int dk, int dv, int C,
+                                        mdn_dtype in_dtype, int flags)
+{
+    (void)flags;
+    return ws_size(Sizes{B, T, Hk, H, dk, dv, C, in_dtype, false}, false);
+}
+
+size_t mdn_gdr_chunk_fwd_varlen_workspace_size(int N, int total_T, int Hk, int H, int dk, int dv,
+                                               int C, mdn_dtype in_dtype, int flags)
+{
+    (void)flags;
+    return ws_size(Sizes{N, total_T, Hk, H, dk, dv, C, in_dtype, true}, false);
+}
+
+size_t mdn_gdr_chunk_bwd_workspace_size(int B, int T, int Hk, int H, int dk, int dv, int C,
+                                        mdn_dtype in_dtype, int flags)
+{
+    (void)flags;
+    return ws_size(Sizes{B, T, Hk, H, dk, dv, C, in_dtype, false}, true);
+}
+
+size_t mdn_gdr_chunk_bwd_varlen_workspace_size(int N, int total_T, int Hk, int H, int dk, int dv,
+                                               int C, mdn_dtype in_dtype, int flags)
+{
+    (void)flags;
+    return ws_size(Sizes{N, total_T, Hk, H, dk, dv, C, in_dtype, true}, true);
+}
+
+mdn_status mdn_gdr_chunk_fwd(const void* q, const void* k, const void* v, mdn_dtype in_dtype,
+                             const float* alpha_log, const float* beta, float scale,
+                             const float* S0, int B, int T, int Hk, int H, int dk, int dv, int C,
+                             void* o, void* vtilde, float* S_T, void* workspace, size_t ws_bytes,
+                             int flags, mdn_stream_t stream)
+{
+    return fwd_impl(Sizes{B, T, Hk, H, dk, dv, C, in_dtype, false}, q, k, v, alpha_log, beta,
+                    scale, nullptr, S0, o, vtilde, S_T, workspace, ws_bytes, flags, stream);
+}
+
+mdn_status mdn_gdr_chunk_fwd_varlen(const void* q, const void* k, const void* v,
+                                    mdn_dtype in_dtype, const float* alpha_log, const float* beta,
+                                    float scale, const int* cu_seqlens, int N, int total_T,
+                                    const float* S0, int Hk, int H, int dk, int dv, int C, void* o,
+                                    void* vtilde, float* S_T, void* workspace, size_t ws_bytes,
+                                    int flags, mdn_stream_t stream)
+{
+    return fwd_impl(Sizes{N, total_T, Hk, H, dk, dv, C, in_dtype, true}, q, k, v, alpha_log, beta,
+                    scale, cu_seqlens, S0, o, vtilde, S_T, workspace, ws_bytes, flags, stream);
+}
+
+mdn_status mdn_gdr_chunk_bwd(const void* q, const void* k, mdn_dtype in_dtype,
+                             const float* alpha_log, const float* beta, float scale,
+                             const float* S0, const void* vtilde, const void* d_o,
+                             const float* dS_T, int B, int T, int Hk, int H, int dk, int dv, int C,
+                             void* dq, void* dk_out, void* dv_out, float* dalpha_log, float* dbeta,
+                             float* dS0, void* workspace, size_t ws_bytes, int flags,
+                             mdn_stream_t stream)
+{
+    return bwd_impl(Sizes{B, T, Hk, H, dk, dv, C, in_dtype, false}, q, k, alpha_log, beta, scale,
+                    nullptr, S0, vtilde, d_o, dS_T, dq, dk_out, dv_out, dalpha_log, dbeta, dS0,
+                    workspace, ws_bytes, flags, stream);
+}
+
+mdn_status mdn_gdr_chunk_bwd_varlen(const void* q, const void* k, mdn_dtype in_dtype,
+                                    const float* alpha_log, const float* beta, float scale,
+                                    const int* cu_seqlens, int N, int total_T, const float* S0,
+                                    const void* vtilde, const void* d_o, const float* dS_T, int Hk,
+                                    int H, int dk, int dv, int C, void* dq, void* dk_out,
+                                    void* dv_out, float* dalpha_log, float* dbeta, float* dS0,
+                                    void* workspace, size_t ws_bytes, int flags,
+                                    mdn_stream_t stream)
+{
+    return bwd_impl(Sizes{N, total_T, Hk, H, dk, dv, C, in_dtype, true}, q, k, alpha_log, beta,
+                    scale, cu_seqlens, S0, vtilde, d_o, dS_T, dq, dk_out, dv_out, dalpha_log,
+                    dbeta, dS0, workspace, ws_bytes, flags, stream);
+}
+
+mdn_status mdn_gdr_step(const void* q, const void* k, const void* v, mdn_dtype in_dtype,
+                        const float* alpha_log, const float* beta, float scale, const float* S,
+                        float* S_out, int B, int Hk, int H, int dk, int dv, void* o, void* vtilde,
+                        int flags, mdn_stream_t stream)
+{
+    mdn_status st = check_sizes(Sizes{B, 1, Hk, H, dk, dv, kChunk, in_dtype, false});
+    if (st != MDN_OK) return st;
+    if (flags != 0 || !std::isfinite(scale)) return MDN_ERR_INVALID_ARG;
+    if (B == 0 || H == 0) return MDN_OK;
+    const void* tok[] = {q, k, v, o};
+    for (const void* p : tok)
+        if (!p || !aligned_elem(p, in_dtype)) return MDN_ERR_INVALID_ARG;
+    if (vtilde && !aligned_elem(vtilde, in_dtype)) return MDN_ERR_INVALID_ARG;
+    if (!alpha_log || !beta || !aligned4(alpha_log) || !aligned4(beta)) return MDN_ERR_INVALID_ARG;
+    if (!S || !S_out || !aligned16(S) || !aligned16(S_out)) return MDN_ERR_INVALID_ARG;
+    const cudaError_t e = gdr::launch_step(q, k, v, in_dtype, alpha_log, beta, scale, S, S_out, B,
+                                           Hk, H, dk, o, vtilde,
+                                           reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MDN_OK : cuda_fail(e);
+}
+
+}  // extern "C"

@@ -325,7 +325,8 @@ __device__ __forceinline__ ChunkOut chunk_out(const ChunkArgs& a, int b, int n)
 enum KernelKind {
     kGatePrep = 0, kIntraSimt, kInterSimt, kOutputSimt, kStep, kFiniteCheck,
     kChunkTc, kIntraTc, kInterTc, kOutputTc, kGateParams, kVarlen, kBwdPrep, kBwdStates,
-    kBwdChain, kBwdStateGrads, kBwdLocal, kBwdChainPrep, kKernelKinds
+    kBwdChain, kBwdStateGrads, kBwdLocal, kBwdChainPrep, kGdrFwdSimt, kGdrBwdStates, kGdrBwdChain,
+    kGdrBwdGrads, kGdrFold, kGdrStep, kGroupNorm, kGroupNormBwd, kKernelKinds
 };
 // Record a start event for a launch of kind k on s (returns a slot, or -1 when
 // timing is off); prof_end records the matching stop event.
@@ -376,13 +377,14 @@ cudaError_t launch_finite_check(const void* x, size_t n, bool bf16, unsigned* fl
                                 cudaStream_t s);
 // Variable-length mode.  Setup: checks cu_seqlens (N+1 device ints: 0, non-
 // decreasing, ending at total_T), writes the checked copy to cu_s and the
-// chunk offsets to cu_c (N+1 each); an invalid cu_seqlens sets *bad and
+// chunk offsets to cu_c (N+1 each); with exact = false the last offset may
+// leave rows behind it; an invalid cu_seqlens sets *bad and
 // makes every sequence empty.  Gather: the chunk-aligned padded inputs
 // (NT*C rows; padding rows are steps that change nothing: k = v = q = 0,
 // alpha = mu = 1, beta = eta = 0).
 cudaError_t launch_varlen_setup(const int* cu_seqlens, int N, int total_T, int NT, int* cu_s,
                                 int* cu_c, int* seq_order, int* chunk_order, unsigned* bad,
-                                cudaStream_t s);
+                                cudaStream_t s, bool exact = true);
 cudaError_t launch_varlen_gather(const void* q, const void* k, const void* v, size_t elt,
                                  const float* alpha_log, const float* mu_log, const float* beta,
                                  const float* eta, const int* cu_s, const int* cu_c, int N, int H,

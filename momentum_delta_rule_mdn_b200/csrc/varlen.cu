@@ -52,7 +52,7 @@ __device__ int block_incl_sum(int x, int* warp_tot, int& total)
 constexpr int kRankMax = 2048;
 
 __global__ void __launch_bounds__(kSetupThreads)
-varlen_setup_kernel(const int* __restrict__ cu, int N, int total_T, int NT, int* __restrict__ cu_s,
+varlen_setup_kernel(const int* __restrict__ cu, int N, int total_T, bool exact, int NT, int* __restrict__ cu_s,
                     int* __restrict__ cu_c, int* __restrict__ seq_order,
                     int* __restrict__ chunk_order, unsigned* __restrict__ bad)
 {
@@ -63,7 +63,7 @@ varlen_setup_kernel(const int* __restrict__ cu, int N, int total_T, int NT, int*
     for (int i = tid; i <= N; i += kSetupThreads) {
         const int x = cu[i];
         if (i == 0 && x != 0) my_bad = 1;
-        if (i == N && x != total_T) my_bad = 1;
+        if (i == N && (exact ? x != total_T : x > total_T)) my_bad = 1;
         if (i < N && cu[i + 1] < x) my_bad = 1;
     }
     const bool any_bad = __syncthreads_or(my_bad) != 0;
@@ -173,10 +173,10 @@ varlen_gather_kernel(const uint4* __restrict__ q, const uint4* __restrict__ k,
 
 cudaError_t launch_varlen_setup(const int* cu_seqlens, int N, int total_T, int NT, int* cu_s,
                                 int* cu_c, int* seq_order, int* chunk_order, unsigned* bad,
-                                cudaStream_t s)
+                                cudaStream_t s, bool exact)
 {
     ProfScope ps(kVarlen, s);
-    varlen_setup_kernel<<<1, kSetupThreads, 0, s>>>(cu_seqlens, N, total_T, NT, cu_s, cu_c,
+    varlen_setup_kernel<<<1, kSetupThreads, 0, s>>>(cu_seqlens, N, total_T, exact, NT, cu_s, cu_c,
                                                      seq_order, chunk_order, bad);
     return cudaGetLastError();
 }

@@ -2,7 +2,7 @@
 // argument validation, workspace layout and kernel dispatch.
 #include <cmath>
 
-#include "gdr_internal.cuh"
+#include "gdr_tc.cuh"
 
 using namespace mdn;
 
@@ -22,6 +22,8 @@ struct Sizes {
     int B, T, Hk, H, dk, dv, C;
     mdn_dtype dt;
     bool packed;
+    int flags;
+    bool tc() const { return dt == MDN_BF16 && !(flags & MDN_FORCE_SIMT); }
     long long rows() const { return packed ? T : (long long)B * T; }
     // chunks of the call: every sequence ends in at most one partial chunk
     long long chunks() const
@@ -46,6 +48,7 @@ mdn_status check_sizes(const Sizes& z)
 
 struct Layout {
     size_t status, cu_s, cu_c, seq_order, chunk_order;
+    size_t blk;                    // forward on the tensor cores
     size_t SS, GG, dvf, dqp, dkp;  // backward
     size_t total;
 };
@@ -59,6 +62,9 @@ Layout layout(const Sizes& z, bool bwd)
         w.cu_c = off;        off += align_up((size_t)(z.B + 1) * sizeof(int));
         w.seq_order = off;   off += align_up((size_t)z.B * sizeof(int));
         w.chunk_order = off; off += align_up((size_t)z.chunks() * sizeof(int));
+    }
+    if (!bwd && z.tc()) {
+        w.blk = off; off += align_up((size_t)z.chunks() * z.H * gdr::kBlkBytes);
     }
     if (bwd) {
         const size_t states = (size_t)z.chunks() * z.H * z.dk * z.dv * sizeof(float);
@@ -98,6 +104,7 @@ mdn_status begin(gdr::Args& a, const Sizes& z, const Layout& w, char* ws, const 
                             /*exact=*/false);
     if (e != cudaSuccess) return cuda_fail(e);
     a.cu_s = cu_s; a.cu_c = cu_c; a.seq_order = seq;
+    a.chunk_order = reinterpret_cast<int*>(ws + w.chunk_order);
     return MDN_OK;
 }
 
@@ -149,8 +156,10 @@ mdn_status fwd_impl(const Sizes& z, const void* q, const void* k, const void* v,
     gdr::Args a;
     a.q = q; a.k = k; a.v = v; a.alpha_log = alpha_log; a.beta = beta; a.scale = scale; a.S0 = S0;
     a.o = o; a.vt = vtilde; a.S_T = S_T;
+    if (w.blk) a.blk = reinterpret_cast<uint8_t*>(ws + w.blk);
     if ((st = begin(a, z, w, ws, cu_seqlens, s)) != MDN_OK) return st;
-    const cudaError_t e = gdr::launch_fwd_simt(a, z.dt, s);
+    // no tokens: S_T = S0, which the CUDA-core kernel's walk over nothing gives
+    const cudaError_t e = z.tc() && z.rows() > 0 ? gdr::launch_fwd_tc(a, s) : gdr::launch_fwd_simt(a, z.dt, s);
     if (e != cudaSuccess) return cuda_fail(e);
     if (!(flags & MDN_CHECK_FINITE)) return MDN_OK;
     const bool bf = z.dt == MDN_BF16;
@@ -219,29 +228,25 @@ extern "C" {
 size_t mdn_gdr_chunk_fwd_workspace_size(int B, int T, int Hk, int H, int dk, int dv, int C,
                                         mdn_dtype in_dtype, int flags)
 {
-    (void)flags;
-    return ws_size(Sizes{B, T, Hk, H, dk, dv, C, in_dtype, false}, false);
+    return ws_size(Sizes{B, T, Hk, H, dk, dv, C, in_dtype, false, flags}, false);
 }
 
 size_t mdn_gdr_chunk_fwd_varlen_workspace_size(int N, int total_T, int Hk, int H, int dk, int dv,
                                                int C, mdn_dtype in_dtype, int flags)
 {
-    (void)flags;
-    return ws_size(Sizes{N, total_T, Hk, H, dk, dv, C, in_dtype, true}, false);
+    return ws_size(Sizes{N, total_T, Hk, H, dk, dv, C, in_dtype, true, flags}, false);
 }
 
 size_t mdn_gdr_chunk_bwd_workspace_size(int B, int T, int Hk, int H, int dk, int dv, int C,
                                         mdn_dtype in_dtype, int flags)
 {
-    (void)flags;
-    return ws_size(Sizes{B, T, Hk, H, dk, dv, C, in_dtype, false}, true);
+    return ws_size(Sizes{B, T, Hk, H, dk, dv, C, in_dtype, false, flags}, true);
 }
 
 size_t mdn_gdr_chunk_bwd_varlen_workspace_size(int N, int total_T, int Hk, int H, int dk, int dv,
                                                int C, mdn_dtype in_dtype, int flags)
 {
-    (void)flags;
-    return ws_size(Sizes{N, total_T, Hk, H, dk, dv, C, in_dtype, true}, true);
+    return ws_size(Sizes{N, total_T, Hk, H, dk, dv, C, in_dtype, true, flags}, true);
 }
 
 mdn_status mdn_gdr_chunk_fwd(const void* q, const void* k, const void* v, mdn_dtype in_dtype,
@@ -250,7 +255,7 @@ mdn_status mdn_gdr_chunk_fwd(const void* q, const void* k, const void* v, mdn_dt
                              void* o, void* vtilde, float* S_T, void* workspace, size_t ws_bytes,
                              int flags, mdn_stream_t stream)
 {
-    return fwd_impl(Sizes{B, T, Hk, H, dk, dv, C, in_dtype, false}, q, k, v, alpha_log, beta,
+    return fwd_impl(Sizes{B, T, Hk, H, dk, dv, C, in_dtype, false, flags}, q, k, v, alpha_log, beta,
                     scale, nullptr, S0, o, vtilde, S_T, workspace, ws_bytes, flags, stream);
 }
 
@@ -261,7 +266,7 @@ mdn_status mdn_gdr_chunk_fwd_varlen(const void* q, const void* k, const void* v,
                                     void* vtilde, float* S_T, void* workspace, size_t ws_bytes,
                                     int flags, mdn_stream_t stream)
 {
-    return fwd_impl(Sizes{N, total_T, Hk, H, dk, dv, C, in_dtype, true}, q, k, v, alpha_log, beta,
+    return fwd_impl(Sizes{N, total_T, Hk, H, dk, dv, C, in_dtype, true, flags}, q, k, v, alpha_log, beta,
                     scale, cu_seqlens, S0, o, vtilde, S_T, workspace, ws_bytes, flags, stream);
 }
 
@@ -273,7 +278,7 @@ mdn_status mdn_gdr_chunk_bwd(const void* q, const void* k, mdn_dtype in_dtype,
                              float* dS0, void* workspace, size_t ws_bytes, int flags,
                              mdn_stream_t stream)
 {
-    return bwd_impl(Sizes{B, T, Hk, H, dk, dv, C, in_dtype, false}, q, k, alpha_log, beta, scale,
+    return bwd_impl(Sizes{B, T, Hk, H, dk, dv, C, in_dtype, false, flags}, q, k, alpha_log, beta, scale,
                     nullptr, S0, vtilde, d_o, dS_T, dq, dk_out, dv_out, dalpha_log, dbeta, dS0,
                     workspace, ws_bytes, flags, stream);
 }
@@ -287,7 +292,7 @@ mdn_status mdn_gdr_chunk_bwd_varlen(const void* q, const void* k, mdn_dtype in_d
                                     void* workspace, size_t ws_bytes, int flags,
                                     mdn_stream_t stream)
 {
-    return bwd_impl(Sizes{N, total_T, Hk, H, dk, dv, C, in_dtype, true}, q, k, alpha_log, beta,
+    return bwd_impl(Sizes{N, total_T, Hk, H, dk, dv, C, in_dtype, true, flags}, q, k, alpha_log, beta,
                     scale, cu_seqlens, S0, vtilde, d_o, dS_T, dq, dk_out, dv_out, dalpha_log,
                     dbeta, dS0, workspace, ws_bytes, flags, stream);
 }
@@ -297,7 +302,7 @@ mdn_status mdn_gdr_step(const void* q, const void* k, const void* v, mdn_dtype i
                         float* S_out, int B, int Hk, int H, int dk, int dv, void* o, void* vtilde,
                         int flags, mdn_stream_t stream)
 {
-    mdn_status st = check_sizes(Sizes{B, 1, Hk, H, dk, dv, kChunk, in_dtype, false});
+    mdn_status st = check_sizes(Sizes{B, 1, Hk, H, dk, dv, kChunk, in_dtype, false, 0});
     if (st != MDN_OK) return st;
     if (flags != 0 || !std::isfinite(scale)) return MDN_ERR_INVALID_ARG;
     if (B == 0 || H == 0) return MDN_OK;

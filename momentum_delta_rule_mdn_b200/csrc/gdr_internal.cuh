@@ -43,6 +43,8 @@ struct Args {
     const int* cu_s = nullptr;
     const int* cu_c = nullptr;
     const int* seq_order = nullptr;
+    const int* chunk_order = nullptr;
+    uint8_t* blk = nullptr;  // tensor-core path: operand blocks of every chunk and head
     // backward
     const void* d_o = nullptr;
     const float* dS_T = nullptr;
@@ -120,6 +122,8 @@ inline long long chains(const Args& a) { return (long long)a.B * a.H; }
 inline long long chunks(const Args& a) { return a.cu_s ? a.NT : (long long)a.B * a.NT; }
 
 // CUDA-core kernels, fp32 arithmetic, any supported type and d.
+// Tensor-core path (bf16).
+cudaError_t launch_fwd_tc(const Args& a, cudaStream_t s);
 cudaError_t launch_fwd_simt(const Args& a, mdn_dtype dt, cudaStream_t s);
 cudaError_t launch_bwd_simt(const Args& a, mdn_dtype dt, cudaStream_t s);
 // Sums of dqp, dkp over the value heads of each key head, in head order.

@@ -326,7 +326,7 @@ enum KernelKind {
     kGatePrep = 0, kIntraSimt, kInterSimt, kOutputSimt, kStep, kFiniteCheck,
     kChunkTc, kIntraTc, kInterTc, kOutputTc, kGateParams, kVarlen, kBwdPrep, kBwdStates,
     kBwdChain, kBwdStateGrads, kBwdLocal, kBwdChainPrep, kGdrFwdSimt, kGdrBwdStates, kGdrBwdChain,
-    kGdrBwdGrads, kGdrFold, kGdrStep, kGroupNorm, kGroupNormBwd, kKernelKinds
+    kGdrBwdGrads, kGdrFold, kGdrStep, kGdrOperands, kGdrChain, kGroupNorm, kGroupNormBwd, kKernelKinds
 };
 // Record a start event for a launch of kind k on s (returns a slot, or -1 when
 // timing is off); prof_end records the matching stop event.

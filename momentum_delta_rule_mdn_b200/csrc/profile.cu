@@ -34,7 +34,7 @@ const char* const kNames[kKernelKinds] = {
     "gate_prep", "intra_simt", "inter_simt", "output_simt", "step", "finite_check",
     "chunk_tc", "intra_tc", "inter_tc", "output_tc", "gate_params", "varlen_prep", "bwd_prep", "bwd_states", "bwd_chain",
     "bwd_state_grads", "bwd_local_grads", "bwd_chain_prep", "gdr_fwd_simt", "gdr_bwd_states",
-    "gdr_bwd_chain", "gdr_bwd_grads", "gdr_fold_heads", "gdr_step", "group_norm", "group_norm_bwd",
+    "gdr_bwd_chain", "gdr_bwd_grads", "gdr_fold_heads", "gdr_step", "gdr_operands", "gdr_chain", "group_norm", "group_norm_bwd",
 };
 
 // Fold every recorded pair into the totals (caller holds the lock).

@@ -172,7 +172,7 @@ def _run_own(s):
     if op == "varlen":
         return dict(zip(("o", "vt", "S"),
                         mdn.gdr_chunk_fwd_varlen(*a, s["cu"], s["scale"], s["S0"])))
-    a, b = a[:2] + a[3:], (s["scale"], s["vt"], s["do"], s["S0"], s["dS_T"])
+    a, b = a[:2] + a[3:], (s["scale"], s["vt"].contiguous(), s["do"], s["S0"], s["dS_T"])
     if op == "chunk_bwd":
         return mdn.gdr_chunk_bwd(*a, *b)
     return mdn.gdr_chunk_bwd_varlen(*a, s["cu"], *b)

@@ -439,7 +439,7 @@ cudaError_t launch_typed(const Args& a, cudaStream_t s)
 }  // namespace
 
 bool make_rows_map(CUtensorMap* map, const void* base, const Args& a, int heads, int box_d,
-                   CUtensorMapSwizzle swizzle)
+                   CUtensorMapSwizzle swizzle, int box_rows)
 {
     auto fn = encode_fn();
     if (!fn) return false;
@@ -447,7 +447,7 @@ bool make_rows_map(CUtensorMap* map, const void* base, const Args& a, int heads,
     const cuuint64_t row = (cuuint64_t)heads * a.D * 2;
     cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)heads, T, B};
     cuuint64_t strides[3] = {(cuuint64_t)a.D * 2, row, T * row};
-    cuuint32_t box[4] = {(cuuint32_t)box_d, 1, (cuuint32_t)kChunk, 1};
+    cuuint32_t box[4] = {(cuuint32_t)box_d, 1, (cuuint32_t)box_rows, 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

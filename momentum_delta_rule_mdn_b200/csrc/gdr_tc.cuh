@@ -44,10 +44,75 @@ __device__ __forceinline__ void split8(const float* x, uint4& hi, uint4& lo)
     lo = tc::bf16x8(l);
 }
 
-// TMA map over [rows..., heads, D] bf16; box = {box_d, 1, 64, 1}.  Batches keep
+// Two values as two bf16 terms each.
+__device__ __forceinline__ void unpack2(uint32_t w, float& x0, float& x1)
+{
+    x0 = __uint_as_float(w << 16);
+    x1 = __uint_as_float(w & 0xffff0000u);
+}
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo)
+{
+    float h0, h1;
+    hi = tc::pack_bf16(x0, x1);
+    unpack2(hi, h0, h1);
+    lo = tc::pack_bf16(x0 - h0, x1 - h1);
+}
+
+// 16 lanes x 8 N columns of TMEM (lanes 32 (warp % 4) .. + 15): thread t holds, of
+// each 8-column piece, columns 2 (t % 4), + 1 of row t / 4 in v[4 i], v[4 i + 1] and of
+// row t / 4 + 8 in v[4 i + 2], v[4 i + 3].  Warp-collective.
+template <int N>
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, float* v)
+{
+    if constexpr (N == 1) {
+        uint32_t r[4];
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(taddr));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
+    } else if constexpr (N == 2) {
+        uint32_t r[8];
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                       "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) tmem_ld_16x256<2>(taddr + 8 * i, v + 4 * i);
+    }
+}
+
+// D[tmem] (+)= A B and its commit, issued by one elected lane of a converged warp: the
+// operands stay in uniform registers, and an instruction is issued every 32 cycles
+// instead of the 54 it takes from inside a one-lane branch.
+__device__ __forceinline__ void mma_bf16_elect(uint32_t d, uint64_t adesc, uint64_t bdesc,
+                                               uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit_elect(uint64_t* bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(
+            sm100::smem_u32(bar))
+        : "memory");
+}
+
+// TMA map over [rows..., heads, D] bf16; box = {box_d, 1, box_rows, 1}.  Batches keep
 // their own dimension so that rows past T read as zeros.
 bool make_rows_map(CUtensorMap* map, const void* base, const Args& a, int heads, int box_d,
-                   CUtensorMapSwizzle swizzle);
+                   CUtensorMapSwizzle swizzle, int box_rows = kChunk);
 
 // The operand blocks of every chunk and head (a.blk).
 cudaError_t launch_operands_tc(const Args& a, cudaStream_t s);

@@ -24,6 +24,7 @@ struct Sizes {
     bool packed;
     int flags;
     bool tc() const { return dt == MDN_BF16 && !(flags & MDN_FORCE_SIMT); }
+    bool bwd_tc() const { return tc() && dk == 128; }
     long long rows() const { return packed ? T : (long long)B * T; }
     // chunks of the call: every sequence ends in at most one partial chunk
     long long chunks() const
@@ -49,7 +50,9 @@ mdn_status check_sizes(const Sizes& z)
 struct Layout {
     size_t status, cu_s, cu_c, seq_order, chunk_order;
     size_t blk;                    // forward on the tensor cores
-    size_t SS, GG, dvf, dqp, dkp;  // backward
+    size_t SS, GG, dvf, dqp, dkp;  // backward on CUDA cores
+    size_t ssf, sb, gb, xs, po, px, pb, pw, gs, dvl;  // backward on the tensor cores
+    int ns;
     size_t total;
 };
 
@@ -66,7 +69,24 @@ Layout layout(const Sizes& z, bool bwd)
     if (!bwd && z.tc()) {
         w.blk = off; off += align_up((size_t)z.chunks() * z.H * gdr::kBlkBytes);
     }
-    if (bwd) {
+    if (bwd && z.bwd_tc()) {
+        const size_t ch = (size_t)z.chunks() * z.H, dd = (size_t)z.dk * z.dv;
+        // 32 columns a slice while four CTAs per chain fit a B200's 148 SMs at once (the
+        // shortest chunk step), else 64 (half the loads of K, Q and the images)
+        w.ns = (long long)z.B * z.H * 4 <= 148 ? 32 : 64;
+        const size_t sl = z.dk / w.ns;
+        w.blk = off; off += align_up(ch * gdr::kBwdBytes);
+        w.ssf = off; off += align_up(ch * dd * sizeof(float));
+        w.sb = off;  off += align_up(ch * dd * 2);
+        w.gb = off;  off += align_up(ch * dd * 2);
+        w.xs = off;  off += align_up(ch * kChunk * z.dk * sizeof(float));
+        w.po = off;  off += align_up(ch * sl * 4 * kChunk * sizeof(float));
+        w.px = off;  off += align_up(ch * sl * 4 * kChunk * sizeof(float));
+        w.pb = off;  off += align_up(ch * sl * 4 * kChunk * sizeof(float));
+        w.pw = off;  off += align_up(ch * sl * 4 * kChunk * sizeof(float));
+        w.gs = off;  off += align_up(ch * sl * 16 * sizeof(float));
+        w.dvl = off; off += align_up((size_t)z.rows() * z.H * z.dk * 2);
+    } else if (bwd) {
         const size_t states = (size_t)z.chunks() * z.H * z.dk * z.dv * sizeof(float);
         const size_t tok = (size_t)z.rows() * z.H * z.dk * sizeof(float);
         w.SS = off;  off += align_up(states);
@@ -201,13 +221,19 @@ mdn_status bwd_impl(const Sizes& z, const void* q, const void* k, const float* a
     a.o = nullptr; a.vt = const_cast<void*>(vtilde); a.S_T = nullptr;
     a.d_o = d_o; a.dS_T = dS_T; a.dq = dq; a.dk = dk_out; a.dv = dv_out;
     a.dalpha_log = dalpha_log; a.dbeta = dbeta; a.dS0 = dS0;
-    a.SS = reinterpret_cast<float*>(ws + w.SS);
-    a.GG = reinterpret_cast<float*>(ws + w.GG);
-    a.dvf = reinterpret_cast<float*>(ws + w.dvf);
-    a.dqp = w.dqp ? reinterpret_cast<float*>(ws + w.dqp) : nullptr;
-    a.dkp = w.dkp ? reinterpret_cast<float*>(ws + w.dkp) : nullptr;
+    auto at = [&](size_t o) { return o ? reinterpret_cast<float*>(ws + o) : nullptr; };
+    a.SS = at(w.SS); a.GG = at(w.GG); a.dvf = at(w.dvf); a.dqp = at(w.dqp); a.dkp = at(w.dkp);
+    a.ns = w.ns;
+    a.blk = reinterpret_cast<uint8_t*>(at(w.blk));
+    a.ssf = at(w.ssf); a.xs = at(w.xs); a.po = at(w.po); a.px = at(w.px); a.pb = at(w.pb);
+    a.pw = at(w.pw); a.gs = at(w.gs);
+    a.sb = reinterpret_cast<__nv_bfloat16*>(at(w.sb));
+    a.gb = reinterpret_cast<__nv_bfloat16*>(at(w.gb));
+    a.dvl = reinterpret_cast<__nv_bfloat16*>(at(w.dvl));
     if ((st = begin(a, z, w, ws, cu_seqlens, s)) != MDN_OK) return st;
-    cudaError_t e = gdr::launch_bwd_simt(a, z.dt, s);
+    // no tokens: dS0 = dS_T, which the CUDA-core chain's walk over nothing gives
+    const bool tc = z.bwd_tc() && z.rows() > 0;
+    cudaError_t e = tc ? gdr::launch_bwd_tc(a, s) : gdr::launch_bwd_simt(a, z.dt, s);
     if (e == cudaSuccess && a.dqp) e = gdr::launch_fold_heads(a, z.dt, s);
     if (e != cudaSuccess) return cuda_fail(e);
     if (!(flags & MDN_CHECK_FINITE)) return MDN_OK;

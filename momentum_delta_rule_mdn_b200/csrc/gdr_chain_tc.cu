@@ -506,7 +506,7 @@ cudaError_t launch_chain(const Args& a, cudaStream_t s)
 // Chain width.  (Figures: see the table in the header comment of launch_fwd_tc.)
 cudaError_t launch_fwd_tc(const Args& a, cudaStream_t s)
 {
-    cudaError_t e = launch_operands_tc(a, s);
+    cudaError_t e = launch_operands_tc(a, s, false);
     if (e != cudaSuccess) return e;
     int dev = 0, sms = 148;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess ||

@@ -1,0 +1,451 @@
+// The backward pass's token gradients of the gated delta rule on sm_100a: one CTA per
+// chunk and key head, summing over the value heads that share it.  With L_{r,i} =
+// exp(la_r - la_i), S the state entering the chunk and G the adjoint of the one leaving,
+//     M1_{r,i} = scale L beta_i (do_r . vtilde_i)   (i <= r)
+//     M2_{r,i} = L beta_i (dv_r . vtilde_i)         (i < r)
+//     dq = Diag(Dq) dO S^T + M1 K
+//     dk = Diag(gam) Vtilde G^T - Diag(D) dv S^T + M1^T Q - M2^T K - M2 K
+// (all heads accumulate in the same two TMEM results), and for the gates
+//     dbeta_r = vtilde_r . dv_r / beta_r                     (from the reverse chain)
+// and dalpha_log_t as the sum of everything whose decay spans token t: with
+// Z_{r,i} = M1_{r,i} q_r.k_i - M2_{r,i} k_r.k_i for i < r,
+//     dalpha_log_t = aC <G, S> + sum_{r >= t} (scale D_r (S^T q_r) . do_r - XS_r . dv_r)
+//                  + sum_{i < t} gam_i (G^T k_i) . vtilde_i + sum_{r >= t > i} Z_{r,i}.
+// The last is a suffix sum of (row sum - column sum) of Z.  (The shorter recurrence
+// dalpha_log_t = dalpha_log_{t+1} + q.dq - beta dbeta - ... adds and later takes off what
+// each token does to itself: with alpha = e^-3 it lost 1.5e-4 of the result.)
+//
+// dq and dk are rounded to bf16, so S, G, M1, M2 and the scaled rows enter as single
+// bf16 terms.  The gate gradients are fp32: their products P1, P2 and [K; Q] K^T have
+// exact bf16 factors, dv in two terms.  P1 = dO Vtilde^T, P2 = dv Vtilde^T.
+//
+// One CTA of 256 threads per SM (176 KB of operands), bound by the latency of its
+// phases: loads, [K; Q] K^T and the P products, the rows of M (warps 0..3) beside the
+// scaling of dO, Vtilde and dv in place (warps 4..7), the products, the stores.
+#include "gdr_tc.cuh"
+
+namespace mdn {
+namespace gdr {
+namespace {
+
+using namespace sm100;
+using namespace tc;
+using inter::wait_bar;
+
+constexpr int D = 128, kThreads = 256;
+constexpr uint32_t KQ = 0;               // [K; Q]: 2 panels of 128 rows
+constexpr uint32_t DV = 32768;           // [dv; dO]: the same
+constexpr uint32_t VT = 65536;           // Vtilde: 2 panels of 64 rows
+constexpr uint32_t DL = VT + 16384;      // dv's second term: the same (and 16 KB more are read behind it)
+constexpr uint32_t SB = DL + 16384;      // S: 2 panels of 128 rows
+constexpr uint32_t GB = SB + 32768;      // G
+constexpr uint32_t M1 = GB + 32768;      // M1, -M2: 64 rows x 128 B
+constexpr uint32_t M2 = M1 + 8192;
+constexpr uint32_t VEC = M2 + 8192;      // gate vectors
+constexpr uint32_t REC = VEC + 1024;     // the chunk's record
+constexpr uint32_t CS = REC + kBwdRecBytes;  // sums of Z: [2][64] rows, [4][64] columns by warp
+constexpr uint32_t BT = CS + 6 * 256;    // [4] block factors
+constexpr uint32_t BARS = BT + 16;
+constexpr uint32_t MISC = BARS + 48;
+constexpr uint32_t BYTES = MISC + 16;
+static_assert(BYTES <= 232448 && BARS % 8 == 0, "shared memory");
+// TMEM: [K; Q] K^T 64, [P2; P1] 64, P2's second term 64, then dq 128, dk 128
+constexpr uint32_t TM_G = 0, TM_P = 64, TM_PL = 128, TM_Q = 256, TM_K = 384;
+
+struct GradMaps {
+    CUtensorMap q, k, vt, d_o, dv, dvl, s, g, dq, dk;
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+grads_kernel(const __grid_constant__ GradMaps tm, const Args a)
+{
+    extern __shared__ __align__(1024) uint8_t sm[];
+    const uint32_t sbase = smem_u32(sm);
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int quad = warp & 3;
+    const long long n = blockIdx.x / a.Hk;
+    const int hk = blockIdx.x % a.Hk, rep = a.H / a.Hk;
+    const ChunkRows cr = chunk_rows(a, n);
+    if (cr.valid <= 0) return;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + BARS);  // [0] K, Q; [1] rows; [2] S, G; [3] P; [4] sums
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + MISC + 4);
+    const int tb = a.cu_s ? 0 : (int)(n / a.NT);
+    const int tt = a.cu_s ? (int)cr.row0 : (int)(n % a.NT) * kChunk;
+    const int SL = D / a.ns;
+
+    if (tid == 0) {
+        for (int k = 0; k < 5; ++k) mbar_init(&bars[k], 1);
+        mbar_fence_init();
+        *abort_flag = 0;
+    }
+    if (warp == 0) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    for (int e = tid; e < 16384 / 16; e += kThreads)  // M above the diagonal blocks stays zero
+        *reinterpret_cast<uint4*>(sm + M1 + 16 * e) = make_uint4(0, 0, 0, 0);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t tq = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+
+    auto load_rows = [&](int h) {
+        mbar_arrive_expect_tx(&bars[1], 4 * 16384);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            tma_load_4d(sm + DV + p * 16384, &tm.dv, p * 64, h, tt, tb, &bars[1]);
+            tma_load_4d(sm + DV + p * 16384 + 8192, &tm.d_o, p * 64, h, tt, tb, &bars[1]);
+            tma_load_4d(sm + VT + p * 8192, &tm.vt, p * 64, h, tt, tb, &bars[1]);
+            tma_load_4d(sm + DL + p * 8192, &tm.dvl, p * 64, h, tt, tb, &bars[1]);
+        }
+    };
+    auto load_states = [&](int h) {
+        mbar_arrive_expect_tx(&bars[2], 65536);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            tma_load_3d(sm + SB + p * 16384, &tm.s, p * 64, 0, (int)(n * a.H + h), &bars[2]);
+            tma_load_3d(sm + GB + p * 16384, &tm.g, p * 64, 0, (int)(n * a.H + h), &bars[2]);
+        }
+    };
+    int loads = 0;  // heads whose loads were issued (thread 0), to drain after an abort
+    if (tid == 0) {
+        mbar_arrive_expect_tx(&bars[0], 32768);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            tma_load_4d(sm + KQ + p * 16384, &tm.k, p * 64, hk, tt, tb, &bars[0]);
+            tma_load_4d(sm + KQ + p * 16384 + 8192, &tm.q, p * 64, hk, tt, tb, &bars[0]);
+        }
+        load_rows(hk * rep);
+        load_states(hk * rep);
+        loads = 1;
+    }
+    const GateVec gv{sm + VEC, 16};
+    float* bt = reinterpret_cast<float*>(sm + BT);
+    float* rec = reinterpret_cast<float*>(sm + REC);
+    float* cs = reinterpret_cast<float*>(sm + CS);
+
+    bool ok = wait_bar(&bars[0], 0, abort_flag);
+    if (a.cu_s && cr.valid < kChunk) {
+        // K and Q rows behind the sequence meet zeros of M: make them zero
+        for (int e = tid; e < 128 * 16; e += kThreads) {
+            const int r = e >> 4, p = e & 15;
+            if ((r & 63) >= cr.valid)
+                *reinterpret_cast<uint4*>(sm + KQ + (p >> 3) * 16384 + sw128_off(r, p & 7)) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+    }
+    ok = __syncthreads_and(ok);
+    if (ok) {
+        if (warp == 0) {  // [K; Q] K^T
+            constexpr uint32_t id = idesc_bf16(128, 64, false, false);
+            const uint64_t d0 = smem_desc(sbase + KQ, 16, 1024, kSw128);
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+                const uint64_t d = d0 + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4);
+                mma_bf16_elect(tmem + TM_G, d, d, id, ks > 0);
+            }
+        }
+        for (int hh = 0; hh < rep; ++hh) {
+            const int h = hk * rep + hh;
+            const size_t hcn = (size_t)n * a.H + h;
+            if (warp == 4) {  // gates of the head
+                float ga[2], gb[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int t = 2 * lane + e;
+                    const bool in = t < cr.valid;
+                    ga[e] = in ? a.alpha_log[(cr.row0 + t) * a.H + h] : 0.f;
+                    gb[e] = in ? a.beta[(cr.row0 + t) * a.H + h] : 0.f;
+                }
+                scan_gates<false>(gv, bt, nullptr, a.scale, ga, gb, lane);
+            } else if (warp == 5) {
+                const float4* src = reinterpret_cast<const float4*>(a.blk + hcn * kBwdBytes + kBwdImg);
+                for (int e = lane; e < (int)kBwdRecBytes / 16; e += 32) reinterpret_cast<float4*>(rec)[e] = src[e];
+            }
+            if (warp == 0) {
+                ok = wait_bar(&bars[1], hh & 1, abort_flag);
+                tc_fence_after_sync();
+                __syncwarp();
+                constexpr uint32_t id = idesc_bf16(128, 64, false, false);
+                const uint64_t da = smem_desc(sbase + DV, 16, 1024, kSw128);
+                const uint64_t db = smem_desc(sbase + VT, 16, 1024, kSw128);
+                const uint64_t dl = smem_desc(sbase + DL, 16, 1024, kSw128);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) {
+                    const uint32_t ka = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
+                    const uint32_t kb = ((ks >> 2) * 8192 + (ks & 3) * 32) >> 4;
+                    mma_bf16_elect(tmem + TM_P, da + ka, db + kb, id, ks > 0);
+                    // lanes 0..63 only: rows 64.. of this operand are whatever lies behind it
+                    mma_bf16_elect(tmem + TM_PL, dl + kb, db + kb, id, ks > 0);
+                }
+                mma_commit_elect(&bars[3]);
+            }
+            ok = wait_bar(&bars[3], hh & 1, abort_flag) && ok;
+            if (!(ok = __syncthreads_and(ok))) break;
+            tc_fence_after_sync();
+            if (warp < 4) {
+                // ---- rows of -M2 (lanes 0..63) and M1, and their sums for dalpha_log
+                const int r = tid & 63, R = r >> 4;
+                const bool m1 = warp >= 2, live = r < cr.valid;
+                const float ph = gv.at(kP, r), pl = gv.at(kPlo, r), lead = m1 ? a.scale : 1.f;
+                float fd[16];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const float4 p4 = gv.get4(kP, 4 * R + g), l4 = gv.get4(kPlo, 4 * R + g);
+                    const float4 b4 = gv.get4(kBeta, 4 * R + g);
+                    const float pv[4] = {p4.x, p4.y, p4.z, p4.w}, lv[4] = {l4.x, l4.y, l4.z, l4.w};
+                    const float bv[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) fd[4 * g + e] = lead * bv[e] * __expf((ph - pv[e]) + (pl - lv[e]));
+                }
+                const float ep = expf(ph);
+                float off = lead * fmaf(ep, pl, ep), sum = 0.f;
+                const int last = r & 15;
+                uint8_t* dst = sm + (m1 ? M1 : M2);
+#pragma unroll
+                for (int I = 3; I >= 0; --I) {
+                    if (I > ((warp & 1) ? 3 : 1)) continue;
+                    float g[16], p[16], q[16];
+                    tmem_ld16(tq + TM_G + 16 * I, g);
+                    tmem_ld16(tq + TM_P + 16 * I, p);
+                    tmem_ld16(tq + TM_PL + 16 * I, q);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const float4 s4 = gv.get4(kSbeta, 4 * I + x);
+                        const float sv[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = 4 * x + e;
+                            const float f = I == R ? fd[j] : off * sv[e];
+                            const bool in = live && (I < R || (I == R && (m1 ? j <= last : j < last)));
+                            const float t = m1 ? p[j] : p[j] + q[j];
+                            p[j] = in ? (m1 ? f * t : -f * t) : 0.f;
+                            // Z, without the diagonal (M1's own: a token's decay does not act on itself)
+                            g[j] = I < R || (I == R && j < last) ? (live ? p[j] * g[j] : 0.f) : 0.f;
+                            sum += g[j];
+                        }
+                    }
+                    if (I < R) off *= bt[I];
+                    st_bf16x8(dst + sw128_off(r, 2 * I), p);
+                    st_bf16x8(dst + sw128_off(r, 2 * I + 1), p + 8);
+                    // column sums over the warp's 32 rows: halve the columns a lane holds per step
+#pragma unroll
+                    for (int w = 8; w >= 1; w >>= 1) {
+                        const bool up = lane & w;
+#pragma unroll
+                        for (int j = 0; j < w; ++j) {
+                            const float other = __shfl_xor_sync(0xffffffffu, up ? g[j] : g[j + w], w);
+                            g[j] = (up ? g[j + w] : g[j]) + other;
+                        }
+                    }
+                    g[0] += __shfl_xor_sync(0xffffffffu, g[0], 16);
+                    if (lane < 16) cs[128 + 64 * warp + 16 * I + lane] = g[0];
+                }
+                // columns right of the warp's rows
+                if (!(warp & 1)) cs[128 + 64 * warp + 32 + lane] = 0.f;
+                cs[(m1 ? 0 : 64) + r] = sum;
+                tc_fence_before_sync();
+            } else {
+                // ---- Diag(D) dv (negated), Diag(Dq) dO, Diag(gam) Vtilde in place
+                const int t = tid - 128;
+#pragma unroll 4
+                for (int e = t; e < 3 * 64 * 16; e += 128) {
+                    const int which = e >> 10, r = (e >> 4) & 63, c = e & 15;
+                    uint8_t* at = which == 0   ? sm + DV + (c >> 3) * 16384 + sw128_off(r, c & 7)
+                                  : which == 1 ? sm + DV + 8192 + (c >> 3) * 16384 + sw128_off(r, c & 7)
+                                               : sm + VT + (c >> 3) * 8192 + sw128_off(r, c & 7);
+                    const float f = which == 0 ? -rec[kRecD + r] : which == 1 ? rec[kRecDq + r] : rec[kRecGam + r];
+                    float x[8];
+                    unpack_bf16x8(*reinterpret_cast<const uint4*>(at), x);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) x[k] *= f;
+                    st_bf16x8(at, x);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncthreads();
+            tc_fence_after_sync();
+            if (warp == 0) {
+                ok = wait_bar(&bars[2], hh & 1, abort_flag);
+                __syncwarp();
+                constexpr uint32_t ids = idesc_bf16(64, 128, false, false);   // rows . state^T
+                constexpr uint32_t idm = idesc_bf16(64, 128, false, true);    // M . rows
+                constexpr uint32_t idt = idesc_bf16(64, 128, true, true);     // M^T . rows
+                const uint64_t dv = smem_desc(sbase + DV, 16, 1024, kSw128), dO_ = dv + (8192 >> 4);
+                const uint64_t vt = smem_desc(sbase + VT, 16, 1024, kSw128);
+                const uint64_t ds = smem_desc(sbase + SB, 16, 1024, kSw128);
+                const uint64_t dg = smem_desc(sbase + GB, 16, 1024, kSw128);
+                const uint64_t km = smem_desc(sbase + KQ, 16384, 1024, kSw128);         // K, Q as B, MN-major
+                const uint64_t qm = smem_desc(sbase + KQ + 8192, 16384, 1024, kSw128);
+                const uint64_t m1 = smem_desc(sbase + M1, 16, 1024, kSw128), m1t = smem_desc(sbase + M1, 8192, 1024, kSw128);
+                const uint64_t m2 = smem_desc(sbase + M2, 16, 1024, kSw128), m2t = smem_desc(sbase + M2, 8192, 1024, kSw128);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) {
+                    const uint32_t ka = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
+                    const uint32_t kb = ((ks >> 2) * 8192 + (ks & 3) * 32) >> 4;
+                    mma_bf16_elect(tmem + TM_Q, dO_ + ka, ds + ka, ids, hh > 0 || ks > 0);
+                    mma_bf16_elect(tmem + TM_K, dv + ka, ds + ka, ids, hh > 0 || ks > 0);
+                    mma_bf16_elect(tmem + TM_K, vt + kb, dg + ka, ids, 1);
+                }
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) {
+                    mma_bf16_elect(tmem + TM_Q, m1 + ks * 2, km + ks * 128, idm, 1);
+                    mma_bf16_elect(tmem + TM_K, m2 + ks * 2, km + ks * 128, idm, 1);
+                    mma_bf16_elect(tmem + TM_K, m2t + ks * 128, km + ks * 128, idt, 1);
+                    mma_bf16_elect(tmem + TM_K, m1t + ks * 128, qm + ks * 128, idt, 1);
+                }
+                mma_commit_elect(&bars[4]);
+            } else if (warp == 1) {
+                // ---- the head's gate gradients
+                float c[2] = {0.f, 0.f}, b[2] = {0.f, 0.f}, w_[2] = {0.f, 0.f};
+                const float2* po = reinterpret_cast<const float2*>(a.po + hcn * SL * 4 * kChunk);
+                const float2* px = reinterpret_cast<const float2*>(a.px + hcn * SL * 4 * kChunk);
+                const float2* pb = reinterpret_cast<const float2*>(a.pb + hcn * SL * 4 * kChunk);
+                const float2* pw = reinterpret_cast<const float2*>(a.pw + hcn * SL * 4 * kChunk);
+                for (int k = 0; k < 4 * SL; ++k) {
+                    const float2 u = po[k * 32 + lane], v = px[k * 32 + lane], w = pb[k * 32 + lane];
+                    const float2 y = pw[k * 32 + lane];
+                    c[0] += u.x - v.x; c[1] += u.y - v.y;
+                    b[0] += w.x; b[1] += w.y;
+                    w_[0] += y.x; w_[1] += y.y;
+                }
+                float end = 0.f;
+                for (int k = lane; k < 16 * SL; k += 32) end += a.gs[hcn * SL * 16 + k];
+#pragma unroll
+                for (int o = 16; o; o >>= 1) end += __shfl_xor_sync(0xffffffffu, end, o);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 2 * lane + e;
+                    c[e] += (cs[r] + cs[64 + r]) -
+                            ((cs[128 + r] + cs[192 + r]) + (cs[256 + r] + cs[320 + r]));
+                    if (r >= cr.valid) c[e] = w_[e] = 0.f;
+                }
+                float pre = w_[0] + w_[1];  // inclusive prefix sum over lanes
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float y = __shfl_up_sync(0xffffffffu, pre, o);
+                    if (lane >= o) pre += y;
+                }
+                pre -= w_[0] + w_[1];       // of the tokens before this lane's
+                float s = c[0] + c[1];  // inclusive suffix sum over lanes
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float y = __shfl_down_sync(0xffffffffu, s, o);
+                    if (lane + o < 32) s += y;
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 2 * lane + e;
+                    if (r < cr.valid) {
+                        const size_t at = (size_t)(cr.row0 + r) * a.H + h;
+                        float y = (e == 0 ? s : s - c[0]) + (e == 0 ? pre : pre + w_[0]) + end;
+                        // nothing enters a sequence's first token from no state: its decay has no effect
+                        if (r == 0 && cr.first && !a.S0) y = 0.f;
+                        a.dalpha_log[at] = y;
+                        a.dbeta[at] = b[e];
+                    }
+                }
+            }
+            ok = wait_bar(&bars[4], hh & 1, abort_flag) && ok;
+            if (!(ok = __syncthreads_and(ok))) break;
+            tc_fence_after_sync();
+            if (tid == 0 && hh + 1 < rep) {
+                load_rows(h + 1);
+                load_states(h + 1);
+                loads = hh + 2;
+            }
+        }
+    }
+    if (ok) {
+        // ---- dq, dk: bf16 through the rows' tile, 64 columns of 16 rows a warp
+        const int r0 = quad * 16 + (lane >> 2), pc = (lane & 3) * 4, half = warp >> 2;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            float x[32];
+            tmem_ld_16x256<8>(tq + (w ? TM_K : TM_Q) + 64 * half, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    *reinterpret_cast<uint32_t*>(sm + DV + w * 16384 + half * 8192 + sw128_off(r0 + 8 * e, c) + pc) =
+                        pack_bf16(x[4 * c + 2 * e], x[4 * c + 2 * e + 1]);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before_sync();
+        __syncthreads();
+        if (!a.cu_s || cr.valid == kChunk) {
+            if (tid == 0) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    tma_store_4d(&tm.dq, p * 64, hk, tt, tb, sm + DV + p * 8192);
+                    tma_store_4d(&tm.dk, p * 64, hk, tt, tb, sm + DV + 16384 + p * 8192);
+                }
+                bulk_commit_group();
+                bulk_wait_group_all();
+            }
+        } else {
+            for (int e = tid; e < 2 * 64 * 16; e += kThreads) {
+                const int w = e >> 10, r = (e >> 4) & 63, c = e & 15;
+                if (r < cr.valid)
+                    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(w ? a.dk : a.dq) +
+                                              ((size_t)(cr.row0 + r) * a.Hk + hk) * D + 8 * c) =
+                        *reinterpret_cast<const uint4*>(sm + DV + w * 16384 + (c >> 3) * 8192 + sw128_off(r, c & 7));
+            }
+        }
+    } else if (tid == 0) {
+        // after an abort: copies in flight land before shared memory is released
+        (void)mbar_wait(&bars[0], 0);
+        (void)mbar_wait(&bars[1], (loads - 1) & 1);
+        (void)mbar_wait(&bars[2], (loads - 1) & 1);
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (tid == 0 && *abort_flag) atomicOr(a.status + 1, 1u);
+    if (warp == 0) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// [chunks * H] matrices d x d, bf16; box = {64, 128, 1}
+bool make_state_map(CUtensorMap* map, const void* base, const Args& a)
+{
+    return make_chunk_map(map, base, chunks(a) * a.H, D, D, D);
+}
+
+}  // namespace
+
+cudaError_t launch_rebuild_tc(const Args& a, int ns, cudaStream_t s);
+cudaError_t launch_reverse_tc(const Args& a, int ns, cudaStream_t s);
+
+cudaError_t launch_bwd_tc(const Args& a, cudaStream_t s)
+{
+    cudaError_t e;
+    if ((e = launch_operands_tc(a, s, true)) != cudaSuccess) return e;
+    if ((e = launch_rebuild_tc(a, a.ns, s)) != cudaSuccess) return e;
+    if ((e = launch_reverse_tc(a, a.ns, s)) != cudaSuccess) return e;
+    const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    GradMaps m;
+    if (!make_rows_map(&m.q, a.q, a, a.Hk, 64, sw) || !make_rows_map(&m.k, a.k, a, a.Hk, 64, sw) ||
+        !make_rows_map(&m.vt, a.vt, a, a.H, 64, sw) || !make_rows_map(&m.d_o, a.d_o, a, a.H, 64, sw) ||
+        !make_rows_map(&m.dv, a.dv, a, a.H, 64, sw) || !make_rows_map(&m.dvl, a.dvl, a, a.H, 64, sw) ||
+        !make_rows_map(&m.dq, a.dq, a, a.Hk, 64, sw) || !make_rows_map(&m.dk, a.dk, a, a.Hk, 64, sw) ||
+        !make_state_map(&m.s, a.sb, a) || !make_state_map(&m.g, a.gb, a))
+        return cudaErrorInvalidValue;
+    if ((e = cudaFuncSetAttribute(grads_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)BYTES)) !=
+        cudaSuccess)
+        return e;
+    const long long blocks = chunks(a) * a.Hk;
+    if (blocks == 0) return cudaSuccess;
+    ProfScope ps(kGdrBwdGrads, s);
+    grads_kernel<<<(unsigned)blocks, kThreads, BYTES, s>>>(m, a);
+    return cudaGetLastError();
+}
+
+}  // namespace gdr
+}  // namespace mdn

@@ -57,6 +57,18 @@ struct Args {
     float* SS = nullptr;     // [chunks, H, D, D]  S entering each chunk
     float* GG = nullptr;     // [chunks, H, D, D]  adjoint of S leaving each chunk
     float* dvf = nullptr;    // [rows, H, D]  dv in fp32
+    // backward on the tensor cores, per chunk and head (SL = d / ns column slices)
+    int ns = 0;                      // columns per slice
+    float* ssf = nullptr;            // [SL][16 warps][ns / 4][32]  entering state, in thread order
+    __nv_bfloat16* sb = nullptr;     // [d, d]  entering state
+    __nv_bfloat16* gb = nullptr;     // [d, d]  adjoint of the leaving state
+    float* xs = nullptr;             // [SL][64][ns]  Diag(D) K S
+    float* po = nullptr;             // [SL][4][64]  scale D_r (S^T q_r) . do_r over 1/4 of the slice
+    float* px = nullptr;             // [SL][4][64]  XS . dv
+    float* pb = nullptr;             // [SL][4][64]  vtilde . dv / beta  (dbeta)
+    float* pw = nullptr;             // [SL][4][64]  gam_r (G^T k_r) . vtilde_r
+    float* gs = nullptr;             // [SL][16]  aC <G, S>
+    __nv_bfloat16* dvl = nullptr;    // [rows, H, D]  dv - bf16(dv)
     float* dqp = nullptr;    // [rows, H, D]  dq, dk of each value head (H > Hk), else null
     float* dkp = nullptr;
 };
@@ -124,6 +136,7 @@ inline long long chunks(const Args& a) { return a.cu_s ? a.NT : (long long)a.B *
 // CUDA-core kernels, fp32 arithmetic, any supported type and d.
 // Tensor-core path (bf16).
 cudaError_t launch_fwd_tc(const Args& a, cudaStream_t s);
+cudaError_t launch_bwd_tc(const Args& a, cudaStream_t s);
 cudaError_t launch_fwd_simt(const Args& a, mdn_dtype dt, cudaStream_t s);
 cudaError_t launch_bwd_simt(const Args& a, mdn_dtype dt, cudaStream_t s);
 // Sums of dqp, dkp over the value heads of each key head, in head order.

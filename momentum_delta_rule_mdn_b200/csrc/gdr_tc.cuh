@@ -31,7 +31,21 @@ constexpr int kRecD = 0;      // D_r
 constexpr int kRecDq = 64;    // scale D_r
 constexpr int kRecGam = 128;  // gam_r
 constexpr int kRecB = 192;    // [192]: aC
-constexpr int kRecFloats = 256;
+
+// The backward pass's block.  Its chain carries E = dv / beta (finite where beta = 0,
+// and dbeta = vtilde . E): with A'_{r,i} = beta_r L_{r,i} k_r.k_i (the row's beta) and
+// Att'_{r,i} = scale L_{r,i} q_r.k_i,
+//     E = T'^T (Att'^T dO + Diag(gamU) K G),   T' = (I + A')^{-1},   dv = beta E,
+//     G <- aC G + Q^T Diag(Dq) dO - K^T Diag(D) dv,   gamU_i = exp(la_C - la_i).
+// Everything here leads to fp32 gradients (of the gates and the entering state), so
+// Att' is kept in two bf16 terms too.
+constexpr uint32_t kBwdAttLo = 24576;
+constexpr uint32_t kBwdImg = 32768;
+constexpr uint32_t kBwdRecBytes = 1792;
+constexpr uint32_t kBwdBytes = kBwdImg + kBwdRecBytes;
+constexpr int kRecGamU = 192;  // exp(la_C - la_r)
+constexpr int kRecBeta = 256;  // beta_r
+constexpr int kRecBwdB = 320;  // [320]: aC
 
 // x as two bf16 terms, eight values: 16 bytes each.
 __device__ __forceinline__ void split8(const float* x, uint4& hi, uint4& lo)
@@ -109,13 +123,97 @@ __device__ __forceinline__ void mma_commit_elect(uint64_t* bar)
         : "memory");
 }
 
+// a + b exactly, as a float and its rounding error
+__device__ __forceinline__ float two_sum(float x, float y, float& err)
+{
+    const float s = __fadd_rn(x, y), z = __fsub_rn(s, x);
+    err = __fadd_rn(__fsub_rn(x, __fsub_rn(s, z)), __fsub_rn(y, z));
+    return s;
+}
+
+// Gate vectors of a chunk: four vectors of 64 floats, vector v's 4-element piece g at
+// base + (16 v + g) * stride.  p = block sum up to the token (two floats), beta, and
+// beta_i exp(sum behind the token to the end of its block).
+struct GateVec {
+    uint8_t* base;
+    uint32_t stride;
+    __device__ __forceinline__ float4 get4(int v, int g) const {
+        return *reinterpret_cast<const float4*>(base + (16 * v + g) * stride);
+    }
+    __device__ __forceinline__ float& at(int v, int i) const {
+        return *reinterpret_cast<float*>(base + (16 * v + (i >> 2)) * stride + (i & 3) * 4);
+    }
+};
+enum { kP = 0, kPlo = 1, kBeta = 2, kSbeta = 3 };
+
+// One warp: the gate vectors, the block factors and the record of a chunk from
+// its gates (tokens 2 lane, 2 lane + 1).
+// (BWD: the backward block's record, and kSbeta without beta_i.)
+template <bool BWD>
+__device__ __forceinline__ void scan_gates(const GateVec& gv, float* btot, float* rec, float scale,
+                                           const float (&ga)[2], const float (&gb)[2], int lane)
+{
+    const float a0 = ga[0] < -1e4f ? -1e4f : ga[0], a1 = ga[1] < -1e4f ? -1e4f : ga[1];
+    float s1lo, hi, lo;
+    const float s1 = two_sum(a0, a1, s1lo);
+    hi = s1;
+    lo = s1lo;
+#pragma unroll
+    for (int off = 1; off < 8; off <<= 1) {
+        const float h2 = __shfl_up_sync(0xffffffffu, hi, off, 8), l2 = __shfl_up_sync(0xffffffffu, lo, off, 8);
+        if ((lane & 7) >= off) {
+            float e;
+            hi = two_sum(hi, h2, e);
+            lo += l2 + e;
+        }
+    }
+    float bh = __shfl_up_sync(0xffffffffu, hi, 1, 8), bl = __shfl_up_sync(0xffffffffu, lo, 1, 8);
+    if ((lane & 7) == 0) bh = bl = 0.f;
+    const float th = __shfl_sync(0xffffffffu, hi, 7, 8), tl = __shfl_sync(0xffffffffu, lo, 7, 8);
+    float p[2], plo[2], e0;
+    p[0] = two_sum(bh, a0, e0);
+    plo[0] = bl + e0;
+    p[1] = hi;
+    plo[1] = lo;
+    const int B = lane >> 3;
+    float pre = 0.f, post = 0.f, all = 0.f;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        const float t = __shfl_sync(0xffffffffu, th, 8 * b);
+        if (b < B) pre += t;
+        if (b > B) post += t;
+        all += t;
+    }
+    const float fpre = expf(pre), fpost = expf(post);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int r = 2 * lane + e;
+        const float ep = expf(p[e]), D_ = fpre * fmaf(ep, plo[e], ep);
+        const float sx = expf((th - p[e]) + (tl - plo[e])), sb = gb[e] * sx;
+        gv.at(kP, r) = p[e];
+        gv.at(kPlo, r) = plo[e];
+        gv.at(kBeta, r) = gb[e];
+        gv.at(kSbeta, r) = BWD ? sx : sb;
+        if (!rec) continue;
+        rec[kRecD + r] = D_;
+        rec[kRecDq + r] = scale * D_;
+        rec[kRecGam + r] = sb * fpost;
+        if (BWD) {
+            rec[kRecGamU + r] = sx * fpost;
+            rec[kRecBeta + r] = gb[e];
+        }
+    }
+    if ((lane & 7) == 0) btot[B] = expf(th);
+    if (lane == 0 && rec) rec[BWD ? kRecBwdB : kRecB] = expf(all);
+}
+
 // TMA map over [rows..., heads, D] bf16; box = {box_d, 1, box_rows, 1}.  Batches keep
 // their own dimension so that rows past T read as zeros.
 bool make_rows_map(CUtensorMap* map, const void* base, const Args& a, int heads, int box_d,
                    CUtensorMapSwizzle swizzle, int box_rows = kChunk);
 
 // The operand blocks of every chunk and head (a.blk).
-cudaError_t launch_operands_tc(const Args& a, cudaStream_t s);
+cudaError_t launch_operands_tc(const Args& a, cudaStream_t s, bool bwd);
 
 }  // namespace gdr
 }  // namespace mdn

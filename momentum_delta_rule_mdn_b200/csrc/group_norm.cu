@@ -23,6 +23,7 @@
 // summed per thread, per block and then over blocks in a fixed order, so
 // results do not depend on timing.
 #include <algorithm>
+#include <type_traits>
 
 #include "mdn_internal.cuh"
 
@@ -49,25 +50,37 @@ struct Args {
     // workspace
     float* part;   // rows form: [N, blocks, G, 2] (mean, M2) or (sum dh, sum dh xhat)
     float* wpart;  // backward: [partial rows, 2, C]
-    int blocks;    // row blocks per n (rows form) / grid.x (tokens form, backward)
+    int blocks;    // row blocks per n (rows form) / grid.x (tokens form)
     int prows;     // partial rows of wpart
 };
 
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBatch = 4;  // values of a thread in flight at once (rows form)
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
-__device__ __forceinline__ float act_of(float z, int act)
+// 1 / (1 + exp(-z)) by the hardware's approximate exponential and reciprocal (a few
+// 1e-7 relative near 0, |z| 1e-7 in the tails, where the value is small; results below
+// 2^-126 become 0): with the rounded functions the tokens form is bound by issue.
+__device__ __forceinline__ float sigmoid(float z)
 {
-    return act == MDN_ACT_SILU ? z * sigmoid(z) : z;
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
+template <int ACT>
+__device__ __forceinline__ float act_of(float z)
+{
+    return ACT == MDN_ACT_SILU ? z * sigmoid(z) : z;
 }
 // act(z) and its derivative
-__device__ __forceinline__ void act_grad(float z, int act, float& f, float& df)
+template <int ACT>
+__device__ __forceinline__ void act_grad(float z, float& f, float& df)
 {
     f = z;
     df = 1.f;
-    if (act == MDN_ACT_SILU) {
+    if (ACT == MDN_ACT_SILU) {
         const float sg = sigmoid(z);
         f = z * sg;
         df = sg * (1.f + z * (1.f - sg));
@@ -111,12 +124,19 @@ __device__ __forceinline__ void stv(T* p, const float* x)
         *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
     }
 }
-// VEC fp32 values that need only 4-byte alignment (weights)
-template <int VEC>
-__device__ __forceinline__ void ldw(const float* p, float* x)
+
+// VEC elements as loaded, to be widened later: what a prefetch keeps.
+template <typename T, int VEC> struct RawOf { using type = uint4; };
+template <typename T> struct RawOf<T, 1> { using type = T; };
+template <typename T, int VEC>
+__device__ __forceinline__ void ld_raw(const T* p, typename RawOf<T, VEC>::type& r)
 {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) x[e] = p[e];
+    r = *reinterpret_cast<const typename RawOf<T, VEC>::type*>(p);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void widen(const typename RawOf<T, VEC>::type& r, float* x)
+{
+    ldv<T, VEC>(reinterpret_cast<const T*>(&r), x);
 }
 
 // Sum over `lanes` (a power of two) neighbouring lanes, in each of them.
@@ -127,68 +147,121 @@ __device__ __forceinline__ float sum_lanes(float x, int lanes)
 }
 
 // ---------------------------------------------------------------- tokens form (L = 1)
-// `lanes` lanes per (token, group); NV vectors of VEC channels per lane.
-template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(kThreads) tokens_fwd_kernel(const Args a, int lanes)
+// One lane group per (group slot, token slot); a lane keeps its channels, and so
+// its weights, over all tokens it takes.  grid.y tiles the groups, grid.x the
+// tokens.  TOK tokens at a time, so that their loads are in flight together.
+template <typename T, int VEC, int NV, int TOK, int ACT, bool GATE>
+__global__ void __launch_bounds__(kThreads, NV * VEC <= 8 ? 4 : 2) tokens_fwd_kernel(const Args a, int lanes, int gslots)
 {
     const int Cg = a.C / a.G, units = Cg / VEC;
-    const int lane = threadIdx.x % lanes;
-    const long long item = (long long)blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes;
-    const bool live = item < (long long)a.N * a.G;
-    const int g = (int)(item % a.G);
-    const size_t base = (size_t)item * Cg;
-    const T* x = static_cast<const T*>(a.x) + base;
-    float v[NV * VEC], z[NV * VEC];
-    float s = 0.f;
+    const int lane = threadIdx.x % lanes, slot = threadIdx.x / lanes;
+    const int per = kThreads / lanes / gslots;
+    const int g = blockIdx.y * gslots + slot % gslots, ts = slot / gslots;
+    const bool glive = g < a.G;
+    float w[NV * VEC], b[NV * VEC];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int u = i * lanes + lane;
-        if (live && u < units) {
-            ldv<T, VEC>(x + u * VEC, v + i * VEC);
-            if (a.gate) ldv<T, VEC>(static_cast<const T*>(a.gate) + base + u * VEC, z + i * VEC);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) s += v[i * VEC + e];
-        }
+    for (int i = 0; i < NV * VEC; ++i) {
+        const int c = ((i / VEC) * lanes + lane) * VEC + i % VEC;
+        const bool in = a.weight && glive && c < Cg;
+        w[i] = in ? a.weight[(size_t)g * Cg + c] : 1.f;
+        b[i] = in ? a.bias[(size_t)g * Cg + c] : 0.f;
     }
-    const float mean = sum_lanes(s, lanes) / Cg;
-    float q = 0.f;
+    const T* __restrict__ xin = static_cast<const T*>(a.x);
+    const T* __restrict__ gin = static_cast<const T*>(a.gate);
+    T* __restrict__ yout = static_cast<T*>(a.y);
+    const int step = gridDim.x * per;
+    const float inv = 1.f / Cg;
+    using Raw = typename RawOf<T, VEC>::type;
+    Raw xr[TOK][NV], zr[TOK][NV];
+    auto fetch = [&](int n0) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-        if (live && i * lanes + lane < units)
+        for (int t = 0; t < TOK; ++t) {
+            const int n = n0 + t * step + blockIdx.x * per + ts;
+            const size_t at = ((size_t)n * a.G + g) * Cg;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float d = v[i * VEC + e] - mean;
-                q = fmaf(d, d, q);
+            for (int i = 0; i < NV; ++i) {
+                const int u = i * lanes + lane;
+                if (glive && n < a.N && u < units) {
+                    ld_raw<T, VEC>(xin + at + u * VEC, xr[t][i]);
+                    if (GATE) ld_raw<T, VEC>(gin + at + u * VEC, zr[t][i]);
+                }
             }
-    const float rstd = 1.f / sqrtf(sum_lanes(q, lanes) / Cg + a.eps);
-    if (!live) return;
-    if (lane == 0) {
-        a.mean[item] = mean;
-        a.rstd[item] = rstd;
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int u = i * lanes + lane;
-        if (u >= units) continue;
-        float w[VEC], b[VEC], y[VEC];
-        if (a.weight) {
-            ldw<VEC>(a.weight + (size_t)g * Cg + u * VEC, w);
-            ldw<VEC>(a.bias + (size_t)g * Cg + u * VEC, b);
         }
+    };
+    fetch(0);
+    for (int n0 = 0; n0 < a.N; n0 += step * TOK) {  // uniform trip count: shuffles below
+        float v[TOK][NV * VEC], z[TOK][NV * VEC];
+        size_t base[TOK];
+        bool live[TOK];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            float n = (v[i * VEC + e] - mean) * rstd;
-            if (a.weight) n = fmaf(n, w[e], b[e]);
-            y[e] = a.gate ? n * act_of(z[i * VEC + e], a.act) : act_of(n, a.act);
+        for (int t = 0; t < TOK; ++t) {
+            const int n = n0 + t * step + blockIdx.x * per + ts;
+            live[t] = glive && n < a.N;
+            base[t] = ((size_t)n * a.G + g) * Cg;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (live[t] && i * lanes + lane < units) {
+                    widen<T, VEC>(xr[t][i], v[t] + i * VEC);
+                    if (GATE) widen<T, VEC>(zr[t][i], z[t] + i * VEC);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) v[t][i * VEC + e] = 0.f;
+                }
+            }
         }
-        stv<T, VEC>(static_cast<T*>(a.y) + base + u * VEC, y);
+        if (n0 + step * TOK < a.N) fetch(n0 + step * TOK);  // the next tokens, under this work
+        float s[TOK], q[TOK];
+#pragma unroll
+        for (int t = 0; t < TOK; ++t) {
+            s[t] = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV * VEC; ++i) s[t] += v[t][i];
+        }
+        for (int off = 1; off < lanes; off <<= 1)
+#pragma unroll
+            for (int t = 0; t < TOK; ++t) s[t] += __shfl_xor_sync(0xffffffffu, s[t], off);
+#pragma unroll
+        for (int t = 0; t < TOK; ++t) {
+            s[t] *= inv;
+            q[t] = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV * VEC; ++i) {
+                const float d = v[t][i] - s[t];
+                if ((i / VEC) * lanes + lane < units) q[t] = fmaf(d, d, q[t]);
+            }
+        }
+        for (int off = 1; off < lanes; off <<= 1)
+#pragma unroll
+            for (int t = 0; t < TOK; ++t) q[t] += __shfl_xor_sync(0xffffffffu, q[t], off);
+#pragma unroll
+        for (int t = 0; t < TOK; ++t) {
+            if (!live[t]) continue;
+            const float mean = s[t], rstd = 1.f / sqrtf(q[t] * inv + a.eps);
+            if (lane == 0) {
+                const size_t item = (size_t)(n0 + t * step + blockIdx.x * per + ts) * a.G + g;
+                a.mean[item] = mean;
+                a.rstd[item] = rstd;
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int u = i * lanes + lane;
+                if (u >= units) continue;
+                float y[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const int j = i * VEC + e;
+                    const float nn = fmaf((v[t][j] - mean) * rstd, w[j], b[j]);
+                    y[e] = GATE ? nn * act_of<ACT>(z[t][j]) : act_of<ACT>(nn);
+                }
+                stv<T, VEC>(yout + base[t] + u * VEC, y);
+            }
+        }
     }
 }
 
-// One lane group per (group slot, token slot); a lane keeps its channels over
-// all tokens it takes, so dw and db add up in registers.  grid.y tiles the
-// groups, grid.x the tokens.
-template <typename T, int VEC, int NV>
+// The same mapping backward: dw and db add up in registers over a lane's tokens,
+// then over the block's token slots in shared memory.
+template <typename T, int VEC, int NV, int ACT, bool GATE>
 __global__ void __launch_bounds__(kThreads) tokens_bwd_kernel(const Args a, int lanes, int gslots)
 {
     const int Cg = a.C / a.G, units = Cg / VEC;
@@ -209,24 +282,45 @@ __global__ void __launch_bounds__(kThreads) tokens_bwd_kernel(const Args a, int 
             b[i] = a.bias[(size_t)g * Cg + c];
         }
     }
+    const T* __restrict__ xin = static_cast<const T*>(a.x);
+    const T* __restrict__ dyin = static_cast<const T*>(a.dy);
+    const T* __restrict__ gin = static_cast<const T*>(a.gate);
     const int step = gridDim.x * per;
+    const float inv = 1.f / Cg;
+    using Raw = typename RawOf<T, VEC>::type;
+    Raw xr[NV], dr[NV], zr[NV];
+    float mr[2] = {0.f, 0.f};
+    auto fetch = [&](int n) {
+        if (!(glive && n < a.N)) return;
+        const size_t at = ((size_t)n * a.G + g) * Cg;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int u = i * lanes + lane;
+            if (u < units) {
+                ld_raw<T, VEC>(xin + at + u * VEC, xr[i]);
+                ld_raw<T, VEC>(dyin + at + u * VEC, dr[i]);
+                if (GATE) ld_raw<T, VEC>(gin + at + u * VEC, zr[i]);
+            }
+        }
+        mr[0] = a.mean[(size_t)n * a.G + g];
+        mr[1] = a.rstd[(size_t)n * a.G + g];
+    };
+    fetch(prow);
     for (int n0 = 0; n0 < a.N; n0 += step) {  // uniform trip count: shuffles below
         const int n = n0 + prow;
         const bool live = glive && n < a.N;
         const size_t base = ((size_t)n * a.G + g) * Cg;
-        const float mean = live ? a.mean[(size_t)n * a.G + g] : 0.f;
-        const float rstd = live ? a.rstd[(size_t)n * a.G + g] : 0.f;
+        const float mean = mr[0], rstd = mr[1];
         float xh[NV * VEC], dh[NV * VEC], z[NV * VEC];
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int u = i * lanes + lane;
-            if (live && u < units) {
-                ldv<T, VEC>(static_cast<const T*>(a.x) + base + u * VEC, xh + i * VEC);
-                ldv<T, VEC>(static_cast<const T*>(a.dy) + base + u * VEC, dh + i * VEC);
-                if (a.gate) ldv<T, VEC>(static_cast<const T*>(a.gate) + base + u * VEC, z + i * VEC);
+        for (int i = 0; i < NV; ++i)
+            if (live && i * lanes + lane < units) {
+                widen<T, VEC>(xr[i], xh + i * VEC);
+                widen<T, VEC>(dr[i], dh + i * VEC);
+                if (GATE) widen<T, VEC>(zr[i], z + i * VEC);
             }
-        }
+        if (n0 + step < a.N) fetch(n + step);  // the next token, under this one's work
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int u = i * lanes + lane;
@@ -237,8 +331,8 @@ __global__ void __launch_bounds__(kThreads) tokens_bwd_kernel(const Args a, int 
                 const int j = i * VEC + e;
                 const float h = (xh[j] - mean) * rstd, nn = fmaf(h, w[j], b[j]);
                 float f, df, dn;
-                act_grad(a.gate ? z[j] : nn, a.act, f, df);
-                if (a.gate) {
+                act_grad<ACT>(GATE ? z[j] : nn, f, df);
+                if (GATE) {
                     dn = dh[j] * f;
                     dz[e] = dh[j] * nn * df;
                 } else {
@@ -251,9 +345,9 @@ __global__ void __launch_bounds__(kThreads) tokens_bwd_kernel(const Args a, int 
                 s1 += dh[j];
                 s2 = fmaf(dh[j], h, s2);
             }
-            if (a.gate) stv<T, VEC>(static_cast<T*>(a.dgate) + base + u * VEC, dz);
+            if (GATE) stv<T, VEC>(static_cast<T*>(a.dgate) + base + u * VEC, dz);
         }
-        const float m1 = sum_lanes(s1, lanes) / Cg, m2 = sum_lanes(s2, lanes) / Cg;
+        const float m1 = sum_lanes(s1, lanes) * inv, m2 = sum_lanes(s2, lanes) * inv;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int u = i * lanes + lane;
@@ -265,14 +359,148 @@ __global__ void __launch_bounds__(kThreads) tokens_bwd_kernel(const Args a, int 
             stv<T, VEC>(static_cast<T*>(a.dx) + base + u * VEC, dx);
         }
     }
-    if (!a.dweight || !glive) return;
+    if (!a.dweight) return;
+    extern __shared__ float sh[];  // [2 NV VEC][kThreads]
+#pragma unroll
+    for (int i = 0; i < NV * VEC; ++i) {
+        sh[2 * i * kThreads + threadIdx.x] = dw[i];
+        sh[(2 * i + 1) * kThreads + threadIdx.x] = db[i];
+    }
+    __syncthreads();
+    if (ts != 0 || !glive) return;
 #pragma unroll
     for (int i = 0; i < NV * VEC; ++i) {
         const int c = ((i / VEC) * lanes + lane) * VEC + i % VEC;
-        if (c < Cg) {
-            a.wpart[((size_t)prow * 2) * a.C + (size_t)g * Cg + c] = dw[i];
-            a.wpart[((size_t)prow * 2 + 1) * a.C + (size_t)g * Cg + c] = db[i];
+        if (c >= Cg) continue;
+        float x = 0.f, y = 0.f;
+        for (int t = 0; t < per; ++t) {  // token slots in order
+            x += sh[2 * i * kThreads + threadIdx.x + t * gslots * lanes];
+            y += sh[(2 * i + 1) * kThreads + threadIdx.x + t * gslots * lanes];
         }
+        a.wpart[((size_t)blockIdx.x * 2) * a.C + (size_t)g * Cg + c] = x;
+        a.wpart[((size_t)blockIdx.x * 2 + 1) * a.C + (size_t)g * Cg + c] = y;
+    }
+}
+
+// The tokens form for groups of exactly LANES vectors (a power of two: head sizes).
+// The same mapping with nothing left to test per element; 8 of a token's 14 values a
+// thread are otherwise spent on it (issue-bound: 94 us instead of the figure below on
+// 32768 x 2048 gated bf16).
+template <typename T, int LANES, int ACT, bool GATE, bool BWD>
+__global__ void __launch_bounds__(kThreads, BWD ? 2 : 4) tokens_exact_kernel(const Args a, int gslots)
+{
+    constexpr int V = 16 / (int)sizeof(T), Cg = LANES * V;
+    constexpr float inv = 1.f / Cg;
+    const int lane = threadIdx.x % LANES, slot = threadIdx.x / LANES;
+    const int per = kThreads / LANES / gslots;
+    const int g = blockIdx.y * gslots + slot % gslots, ts = slot / gslots;
+    const bool glive = g < a.G;
+    float w[V], b[V], dw[V], db[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        const bool in = a.weight && glive;
+        w[e] = in ? a.weight[(size_t)g * Cg + lane * V + e] : 1.f;
+        b[e] = in ? a.bias[(size_t)g * Cg + lane * V + e] : 0.f;
+        dw[e] = db[e] = 0.f;
+    }
+    const int step = gridDim.x * per;
+    int n = blockIdx.x * per + ts;
+    const size_t hop = (size_t)step * a.G;
+    size_t item = (size_t)n * a.G + g;
+    uint4 xr, zr, dr;
+    float mr = 0.f, rr = 0.f;
+    xr = zr = dr = make_uint4(0, 0, 0, 0);
+    auto fetch = [&](int n_, size_t it) {
+        if (!(glive && n_ < a.N)) return;
+        const size_t at = it * Cg + lane * V;
+        xr = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + at);
+        if (GATE) zr = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.gate) + at);
+        if (BWD) {
+            dr = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.dy) + at);
+            mr = a.mean[it];
+            rr = a.rstd[it];
+        }
+    };
+    fetch(n, item);
+    for (int n0 = 0; n0 < a.N; n0 += step, n += step, item += hop) {  // uniform: shuffles below
+        const bool live = glive && n < a.N;
+        float v[V], z[V], d[V];
+        widen<T, V>(xr, v);
+        if (GATE) widen<T, V>(zr, z);
+        if (BWD) widen<T, V>(dr, d);
+        float mean = mr, rstd = rr;
+        fetch(n + step, item + hop);
+        const size_t at = item * Cg + lane * V;
+        if (!BWD) {
+            float s = 0.f, q = 0.f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) s += v[e];
+#pragma unroll
+            for (int off = 1; off < LANES; off <<= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+            mean = s * inv;
+#pragma unroll
+            for (int e = 0; e < V; ++e) q = fmaf(v[e] - mean, v[e] - mean, q);
+#pragma unroll
+            for (int off = 1; off < LANES; off <<= 1) q += __shfl_xor_sync(0xffffffffu, q, off);
+            rstd = 1.f / sqrtf(q * inv + a.eps);
+            if (!live) continue;
+            if (lane == 0) {
+                a.mean[item] = mean;
+                a.rstd[item] = rstd;
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float nn = fmaf((v[e] - mean) * rstd, w[e], b[e]);
+                v[e] = GATE ? nn * act_of<ACT>(z[e]) : act_of<ACT>(nn);
+            }
+            stv<T, V>(static_cast<T*>(a.y) + at, v);
+        } else {
+            float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float h = (v[e] - mean) * rstd, nn = fmaf(h, w[e], b[e]);
+                float f, df, dn;
+                act_grad<ACT>(GATE ? z[e] : nn, f, df);
+                dn = d[e] * (GATE ? f : df);
+                if (GATE) z[e] = d[e] * nn * df;
+                if (!live) dn = 0.f;
+                dw[e] = fmaf(dn, h, dw[e]);
+                db[e] += dn;
+                v[e] = h;
+                d[e] = dn * w[e];
+                s1 += d[e];
+                s2 = fmaf(d[e], h, s2);
+            }
+#pragma unroll
+            for (int off = 1; off < LANES; off <<= 1) {
+                s1 += __shfl_xor_sync(0xffffffffu, s1, off);
+                s2 += __shfl_xor_sync(0xffffffffu, s2, off);
+            }
+            if (!live) continue;
+            if (GATE) stv<T, V>(static_cast<T*>(a.dgate) + at, z);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] = rstd * (d[e] - s1 * inv - v[e] * (s2 * inv));
+            stv<T, V>(static_cast<T*>(a.dx) + at, v);
+        }
+    }
+    if (!BWD || !a.dweight) return;
+    extern __shared__ float sh[];  // [2 V][kThreads]
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        sh[2 * e * kThreads + threadIdx.x] = dw[e];
+        sh[(2 * e + 1) * kThreads + threadIdx.x] = db[e];
+    }
+    __syncthreads();
+    if (ts != 0 || !glive) return;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        float x = 0.f, y = 0.f;
+        for (int t = 0; t < per; ++t) {  // token slots in order
+            x += sh[2 * e * kThreads + threadIdx.x + t * gslots * LANES];
+            y += sh[(2 * e + 1) * kThreads + threadIdx.x + t * gslots * LANES];
+        }
+        a.wpart[((size_t)blockIdx.x * 2) * a.C + (size_t)g * Cg + lane * V + e] = x;
+        a.wpart[((size_t)blockIdx.x * 2 + 1) * a.C + (size_t)g * Cg + lane * V + e] = y;
     }
 }
 
@@ -292,9 +520,21 @@ __device__ __forceinline__ RowBlock row_block(const Args& a)
     return r;
 }
 
+// (count, mean, M2) of two sets joined into the first.
+__device__ __forceinline__ void join(float& k, float& mean, float& m2, float k2, float e2, float q2)
+{
+    const float t = k + k2, d = e2 - mean;
+    if (t > 0.f) {
+        const float f = k2 / t;
+        m2 += q2 + d * d * k * f;
+        mean += d * f;
+    }
+    k = t;
+}
+
 // Partial statistics.  One warp per (n, group, row block): the lanes take the
 // group's values of the block in turn.
-template <typename T, bool BWD>
+template <typename T, bool BWD, int ACT, bool GATE>
 __global__ void __launch_bounds__(kThreads) rows_part_kernel(const Args a)
 {
     const int Cg = a.C / a.G, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -312,28 +552,30 @@ __global__ void __launch_bounds__(kThreads) rows_part_kernel(const Args a)
     float* out = a.part + (((size_t)n * a.blocks + blockIdx.x) * a.G + g) * 2;
     if constexpr (!BWD) {
         const float shift = cnt > 0 ? ld_elem(x + base) : 0.f;  // the block's first value
-        for (long long i = lane; i < cnt; i += 32) {
-            const float d = ld_elem(x + base + (size_t)r * a.C + c) - shift;
-            p += d;
-            q = fmaf(d, d, q);
-            r += sr; c += sc;
-            if (c >= Cg) { c -= Cg; ++r; }
+        for (long long i = lane; i < cnt; i += 32 * kBatch) {
+            float v[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                v[u] = i + 32 * u < cnt ? ld_elem(x + base + (size_t)r * a.C + c) - shift : 0.f;
+                r += sr; c += sc;
+                if (c >= Cg) { c -= Cg; ++r; }
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                p += v[u];
+                q = fmaf(v[u], v[u], q);
+            }
         }
         // (mean, M2) of the lane's values, joined pairwise over the lanes
         float k = (float)((cnt - lane + 31) / 32);
         if (cnt <= lane) k = 0.f;
         float mean = k > 0.f ? p / k : 0.f, m2 = k > 0.f ? q - p * mean : 0.f;
+#pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const float k2 = __shfl_xor_sync(0xffffffffu, k, off);
             const float e2 = __shfl_xor_sync(0xffffffffu, mean, off);
             const float q2 = __shfl_xor_sync(0xffffffffu, m2, off);
-            const float t = k + k2, d = e2 - mean;
-            if (t > 0.f) {
-                const float f = k2 / t;
-                m2 = m2 + q2 + d * d * k * f;
-                mean = mean + d * f;
-            }
-            k = t;
+            join(k, mean, m2, k2, e2, q2);
         }
         if (lane == 0) {
             out[0] = mean + shift;
@@ -343,18 +585,29 @@ __global__ void __launch_bounds__(kThreads) rows_part_kernel(const Args a)
         const T* dy = static_cast<const T*>(a.dy);
         const T* gate = static_cast<const T*>(a.gate);
         const float mean = a.mean[(size_t)n * a.G + g], rstd = a.rstd[(size_t)n * a.G + g];
-        for (long long i = lane; i < cnt; i += 32) {
-            const size_t at = base + (size_t)r * a.C + c;
-            const float h = (ld_elem(x + at) - mean) * rstd;
-            const float w = a.weight ? a.weight[(size_t)g * Cg + c] : 1.f;
-            const float nn = a.weight ? fmaf(h, w, a.bias[(size_t)g * Cg + c]) : h;
-            float f, df;
-            act_grad(gate ? ld_elem(gate + at) : nn, a.act, f, df);
-            const float dh = ld_elem(dy + at) * (gate ? f : df) * w;
-            p += dh;
-            q = fmaf(dh, h, q);
-            r += sr; c += sc;
-            if (c >= Cg) { c -= Cg; ++r; }
+        for (long long i = lane; i < cnt; i += 32 * kBatch) {
+            float xv[kBatch], dv[kBatch], zv[kBatch], wv[kBatch], bv[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const size_t at = base + (size_t)r * a.C + c;
+                const bool in = i + 32 * u < cnt;
+                xv[u] = in ? ld_elem(x + at) : mean;
+                dv[u] = in ? ld_elem(dy + at) : 0.f;
+                zv[u] = in && GATE ? ld_elem(gate + at) : 0.f;
+                wv[u] = in && a.weight ? a.weight[(size_t)g * Cg + c] : 1.f;
+                bv[u] = in && a.weight ? a.bias[(size_t)g * Cg + c] : 0.f;
+                r += sr; c += sc;
+                if (c >= Cg) { c -= Cg; ++r; }
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const float h = (xv[u] - mean) * rstd;
+                float f, df;
+                act_grad<ACT>(GATE ? zv[u] : fmaf(h, wv[u], bv[u]), f, df);
+                const float dh = i + 32 * u < cnt ? dv[u] * (GATE ? f : df) * wv[u] : 0.f;
+                p += dh;
+                q = fmaf(dh, h, q);
+            }
         }
         p = sum_lanes(p, 32);
         q = sum_lanes(q, 32);
@@ -366,44 +619,53 @@ __global__ void __launch_bounds__(kThreads) rows_part_kernel(const Args a)
 }
 
 // The (n, group) statistics of the block's groups, from all row blocks, in
-// shared memory; forward: mean and rstd, written out by the first row block.
+// shared memory (a warp per group, its lanes over the row blocks); forward: mean
+// and rstd, written out by the first row block.
 template <bool BWD>
 __device__ __forceinline__ void join_parts(const Args& a, int n, int g0, int g1, float2* st)
 {
-    const int Cg = a.C / a.G, per = (a.L + a.blocks - 1) / a.blocks;
-    for (int g = g0 + (int)threadIdx.x; g < g1; g += kThreads) {
-        const float* p = a.part + ((size_t)n * a.blocks * a.G + g) * 2;
+    const int Cg = a.C / a.G, per = (a.L + a.blocks - 1) / a.blocks, lane = threadIdx.x % 32;
+    for (int g = g0 + (int)threadIdx.x / 32; g < g1; g += kThreads / 32) {
+        const float2* p = reinterpret_cast<const float2*>(a.part) + (size_t)n * a.blocks * a.G + g;
         if constexpr (!BWD) {
             float k = 0.f, mean = 0.f, m2 = 0.f;
-            for (int b = 0; b < a.blocks; ++b) {
+            for (int b = lane; b < a.blocks; b += 32) {
                 const int l0 = min(a.L, b * per), l1 = min(a.L, l0 + per);
-                const float k2 = (float)(l1 - l0) * Cg;
-                if (k2 <= 0.f) continue;
-                const float d = p[(size_t)b * a.G * 2] - mean, t = k + k2, f = k2 / t;
-                m2 += p[(size_t)b * a.G * 2 + 1] + d * d * k * f;
-                mean += d * f;
-                k = t;
+                const float2 v = p[(size_t)b * a.G];
+                if (l1 > l0) join(k, mean, m2, (float)(l1 - l0) * Cg, v.x, v.y);
+            }
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const float k2 = __shfl_xor_sync(0xffffffffu, k, off);
+                const float e2 = __shfl_xor_sync(0xffffffffu, mean, off);
+                const float q2 = __shfl_xor_sync(0xffffffffu, m2, off);
+                join(k, mean, m2, k2, e2, q2);
             }
             const float rstd = 1.f / sqrtf(m2 / ((float)a.L * Cg) + a.eps);
-            st[g - g0] = make_float2(mean, rstd);
-            if (blockIdx.x == 0) {
-                a.mean[(size_t)n * a.G + g] = mean;
-                a.rstd[(size_t)n * a.G + g] = rstd;
+            if (lane == 0) {
+                st[g - g0] = make_float2(mean, rstd);
+                if (blockIdx.x == 0) {
+                    a.mean[(size_t)n * a.G + g] = mean;
+                    a.rstd[(size_t)n * a.G + g] = rstd;
+                }
             }
         } else {
             float s = 0.f, q = 0.f;
-            for (int b = 0; b < a.blocks; ++b) {
-                s += p[(size_t)b * a.G * 2];
-                q += p[(size_t)b * a.G * 2 + 1];
+            for (int b = lane; b < a.blocks; b += 32) {
+                const float2 v = p[(size_t)b * a.G];
+                s += v.x;
+                q += v.y;
             }
+            s = sum_lanes(s, 32);
+            q = sum_lanes(q, 32);
             const float m = (float)a.L * Cg;
-            st[g - g0] = make_float2(s / m, q / m);
+            if (lane == 0) st[g - g0] = make_float2(s / m, q / m);
         }
     }
     __syncthreads();
 }
 
-template <typename T>
+template <typename T, int ACT, bool GATE>
 __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(const Args a)
 {
     __shared__ float2 st[kThreads];  // a tile of kThreads channels touches at most as many groups
@@ -417,14 +679,25 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(const Args a)
     const float w = a.weight ? a.weight[c] : 1.f, b = a.weight ? a.bias[c] : 0.f;
     const T* gate = static_cast<const T*>(a.gate);
     size_t at = ((size_t)n * a.L + rb.l0) * a.C + c;
-    for (int l = rb.l0; l < rb.l1; ++l, at += a.C) {
-        const float nn = fmaf((ld_elem(static_cast<const T*>(a.x) + at) - ms.x) * ms.y, w, b);
-        st_elem(static_cast<T*>(a.y) + at,
-                gate ? nn * act_of(ld_elem(gate + at), a.act) : act_of(nn, a.act));
+    for (int l = rb.l0; l < rb.l1; l += kBatch, at += (size_t)kBatch * a.C) {
+        float xv[kBatch], zv[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const bool in = l + u < rb.l1;
+            xv[u] = in ? ld_elem(static_cast<const T*>(a.x) + at + (size_t)u * a.C) : 0.f;
+            zv[u] = in && GATE ? ld_elem(gate + at + (size_t)u * a.C) : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (l + u >= rb.l1) break;
+            const float nn = fmaf((xv[u] - ms.x) * ms.y, w, b);
+            st_elem(static_cast<T*>(a.y) + at + (size_t)u * a.C,
+                    GATE ? nn * act_of<ACT>(zv[u]) : act_of<ACT>(nn));
+        }
     }
 }
 
-template <typename T>
+template <typename T, int ACT, bool GATE>
 __global__ void __launch_bounds__(kThreads) rows_bwd_kernel(const Args a)
 {
     __shared__ float2 st[kThreads];
@@ -441,16 +714,28 @@ __global__ void __launch_bounds__(kThreads) rows_bwd_kernel(const Args a)
     const T* gate = static_cast<const T*>(a.gate);
     float dw = 0.f, db = 0.f;
     size_t at = ((size_t)n * a.L + rb.l0) * a.C + c;
-    for (int l = rb.l0; l < rb.l1; ++l, at += a.C) {
-        const float h = (ld_elem(static_cast<const T*>(a.x) + at) - mean) * rstd;
-        const float nn = fmaf(h, w, b), dy = ld_elem(static_cast<const T*>(a.dy) + at);
-        float f, df;
-        act_grad(gate ? ld_elem(gate + at) : nn, a.act, f, df);
-        const float dn = dy * (gate ? f : df);
-        if (gate) st_elem(static_cast<T*>(a.dgate) + at, dy * nn * df);
-        dw = fmaf(dn, h, dw);
-        db += dn;
-        st_elem(static_cast<T*>(a.dx) + at, rstd * (dn * w - m.x - h * m.y));
+    for (int l = rb.l0; l < rb.l1; l += kBatch, at += (size_t)kBatch * a.C) {
+        float xv[kBatch], dv[kBatch], zv[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const bool in = l + u < rb.l1;
+            xv[u] = in ? ld_elem(static_cast<const T*>(a.x) + at + (size_t)u * a.C) : 0.f;
+            dv[u] = in ? ld_elem(static_cast<const T*>(a.dy) + at + (size_t)u * a.C) : 0.f;
+            zv[u] = in && GATE ? ld_elem(gate + at + (size_t)u * a.C) : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (l + u >= rb.l1) break;
+            const size_t to = at + (size_t)u * a.C;
+            const float h = (xv[u] - mean) * rstd, nn = fmaf(h, w, b);
+            float f, df;
+            act_grad<ACT>(GATE ? zv[u] : nn, f, df);
+            const float dn = dv[u] * (GATE ? f : df);
+            if (GATE) st_elem(static_cast<T*>(a.dgate) + to, dv[u] * nn * df);
+            dw = fmaf(dn, h, dw);
+            db += dn;
+            st_elem(static_cast<T*>(a.dx) + to, rstd * (dn * w - m.x - h * m.y));
+        }
     }
     if (a.dweight) {
         const size_t prow = (size_t)n * a.blocks + blockIdx.x;
@@ -467,7 +752,13 @@ __global__ void __launch_bounds__(1024) wsum_kernel(const Args a)
     const int r0 = threadIdx.x / 32;
     float s = 0.f;
     if (c < 2LL * a.C)
-        for (int r = r0; r < a.prows; r += 32) s += a.wpart[(size_t)r * 2 * a.C + c];
+        for (int r = r0; r < a.prows; r += 32 * 8) {
+            float v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = r + 32 * u < a.prows ? a.wpart[(size_t)(r + 32 * u) * 2 * a.C + c] : 0.f;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) s += v[u];
+        }
     sh[r0][threadIdx.x % 32] = s;
     __syncthreads();
     s = sh[threadIdx.x % 32][r0];
@@ -482,9 +773,9 @@ struct Plan {
     bool tokens;
     bool vec;     // 16-byte vectors (the group's length and the pointers allow them)
     int lanes, nv;
-    int gslots;   // backward, tokens form
-    int blocks;   // row blocks per n (rows), or token blocks (backward, tokens form)
-    int gtiles;   // backward, tokens form
+    int gslots;   // tokens form: group slots of a block, tiles of groups
+    int gtiles;
+    int blocks;   // row blocks per n (rows form), token blocks (tokens form)
     int prows;    // partial rows of dw, db
     size_t part_bytes, bytes;
 };
@@ -503,16 +794,16 @@ Plan plan_of(int N, int L, int C, int G, bool f32, bool vec, bool bwd)
     const int want = 148 * 4;  // blocks that keep every SM busy
     if (p.tokens) {
         p.nv = p.vec ? (p.nv <= 1 ? 1 : 2) : (p.nv <= 4 ? 4 : 8);
-        if (bwd) {
-            const int slots = kThreads / p.lanes;
-            p.gslots = 1;
-            while (p.gslots < slots && p.gslots < G) p.gslots <<= 1;
-            p.gtiles = (G + p.gslots - 1) / p.gslots;
-            const int per = slots / p.gslots;
-            const int most = (N + per - 1) / per;
-            p.blocks = std::max(1, std::min(most, want / p.gtiles));
-            p.prows = p.blocks * per;
-        }
+        const int slots = kThreads / p.lanes;
+        p.gslots = 1;
+        while (p.gslots < slots && p.gslots < G) p.gslots <<= 1;
+        p.gtiles = (G + p.gslots - 1) / p.gslots;
+        const int per = slots / p.gslots;
+        const int most = (N + per - 1) / per;
+        // forward: enough blocks to fill the SMs, several tokens each; backward fewer, since
+        // every block leaves a partial row of dw and db
+        p.blocks = std::max(1, std::min(most, std::max(1, (bwd ? want / 2 : want * 2) / p.gtiles)));
+        p.prows = p.blocks;
     } else {
         // rows per block at least 16: the second pass rereads the partials of every block
         const int ctiles = (C + kThreads - 1) / kThreads;
@@ -530,52 +821,81 @@ size_t workspace_bytes(int N, int L, int C, int G, bool f32, bool bwd)
     return std::max(plan_of(N, L, C, G, f32, true, bwd).bytes, plan_of(N, L, C, G, f32, false, bwd).bytes);
 }
 
-template <typename T>
-cudaError_t fwd_typed(const Args& a0, const Plan& p, cudaStream_t s)
+// The exact tokens form, if the groups are whole vectors of 4..32 lanes.
+template <typename T, int ACT, bool GATE, bool BWD>
+bool launch_exact(const Args& a, const Plan& p, cudaStream_t s)
 {
-    Args a = a0;
+    constexpr int V = 16 / (int)sizeof(T);
+    if (!p.tokens || !p.vec || a.C / a.G != p.lanes * V || p.lanes < 4) return false;
+    const dim3 grid(p.blocks, p.gtiles);
+    const size_t shm = BWD && a.dweight ? (size_t)2 * V * kThreads * sizeof(float) : 0;
+    if (p.lanes == 4) tokens_exact_kernel<T, 4, ACT, GATE, BWD><<<grid, kThreads, shm, s>>>(a, p.gslots);
+    else if (p.lanes == 8) tokens_exact_kernel<T, 8, ACT, GATE, BWD><<<grid, kThreads, shm, s>>>(a, p.gslots);
+    else if (p.lanes == 16) tokens_exact_kernel<T, 16, ACT, GATE, BWD><<<grid, kThreads, shm, s>>>(a, p.gslots);
+    else tokens_exact_kernel<T, 32, ACT, GATE, BWD><<<grid, kThreads, shm, s>>>(a, p.gslots);
+    return true;
+}
+
+template <typename T, int ACT, bool GATE>
+cudaError_t fwd_typed(const Args& a, const Plan& p, cudaStream_t s)
+{
     constexpr int V = 16 / (int)sizeof(T);
     ProfScope ps(kGroupNorm, s);
+    if (launch_exact<T, ACT, GATE, false>(a, p, s)) return cudaGetLastError();
     if (p.tokens) {
-        const int per = kThreads / p.lanes;
-        const long long items = (long long)a.N * a.G;
-        const unsigned grid = (unsigned)((items + per - 1) / per);
-        if (p.vec && p.nv == 1) tokens_fwd_kernel<T, V, 1><<<grid, kThreads, 0, s>>>(a, p.lanes);
-        else if (p.vec) tokens_fwd_kernel<T, V, 2><<<grid, kThreads, 0, s>>>(a, p.lanes);
-        else if (p.nv == 4) tokens_fwd_kernel<T, 1, 4><<<grid, kThreads, 0, s>>>(a, p.lanes);
-        else tokens_fwd_kernel<T, 1, 8><<<grid, kThreads, 0, s>>>(a, p.lanes);
+        const dim3 grid(p.blocks, p.gtiles);
+        if (p.vec && p.nv == 1) tokens_fwd_kernel<T, V, 1, 1, ACT, GATE><<<grid, kThreads, 0, s>>>(a, p.lanes, p.gslots);
+        else if (p.vec) tokens_fwd_kernel<T, V, 2, 1, ACT, GATE><<<grid, kThreads, 0, s>>>(a, p.lanes, p.gslots);
+        else if (p.nv == 4) tokens_fwd_kernel<T, 1, 4, 2, ACT, GATE><<<grid, kThreads, 0, s>>>(a, p.lanes, p.gslots);
+        else tokens_fwd_kernel<T, 1, 8, 1, ACT, GATE><<<grid, kThreads, 0, s>>>(a, p.lanes, p.gslots);
         return cudaGetLastError();
     }
     const dim3 g1(p.blocks, a.N, (a.G + kThreads / 32 - 1) / (kThreads / 32));
-    rows_part_kernel<T, false><<<g1, kThreads, 0, s>>>(a);
+    rows_part_kernel<T, false, ACT, GATE><<<g1, kThreads, 0, s>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    rows_fwd_kernel<T><<<dim3(p.blocks, a.N, (a.C + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);
+    rows_fwd_kernel<T, ACT, GATE><<<dim3(p.blocks, a.N, (a.C + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t bwd_typed(const Args& a0, const Plan& p, cudaStream_t s)
+template <typename T, int ACT, bool GATE>
+cudaError_t bwd_typed(const Args& a, const Plan& p, cudaStream_t s)
 {
-    Args a = a0;
     constexpr int V = 16 / (int)sizeof(T);
     ProfScope ps(kGroupNormBwd, s);
     cudaError_t e;
-    if (p.tokens) {
+    if (launch_exact<T, ACT, GATE, true>(a, p, s)) {
+    } else if (p.tokens) {
         const dim3 grid(p.blocks, p.gtiles);
-        if (p.vec && p.nv == 1) tokens_bwd_kernel<T, V, 1><<<grid, kThreads, 0, s>>>(a, p.lanes, p.gslots);
-        else if (p.vec) tokens_bwd_kernel<T, V, 2><<<grid, kThreads, 0, s>>>(a, p.lanes, p.gslots);
-        else if (p.nv == 4) tokens_bwd_kernel<T, 1, 4><<<grid, kThreads, 0, s>>>(a, p.lanes, p.gslots);
-        else tokens_bwd_kernel<T, 1, 8><<<grid, kThreads, 0, s>>>(a, p.lanes, p.gslots);
+        const size_t shm = a.dweight ? (size_t)2 * p.nv * (p.vec ? V : 1) * kThreads * sizeof(float) : 0;
+        if (p.vec && p.nv == 1) tokens_bwd_kernel<T, V, 1, ACT, GATE><<<grid, kThreads, shm, s>>>(a, p.lanes, p.gslots);
+        else if (p.vec) tokens_bwd_kernel<T, V, 2, ACT, GATE><<<grid, kThreads, shm, s>>>(a, p.lanes, p.gslots);
+        else if (p.nv == 4) tokens_bwd_kernel<T, 1, 4, ACT, GATE><<<grid, kThreads, shm, s>>>(a, p.lanes, p.gslots);
+        else tokens_bwd_kernel<T, 1, 8, ACT, GATE><<<grid, kThreads, shm, s>>>(a, p.lanes, p.gslots);
     } else {
         const dim3 g1(p.blocks, a.N, (a.G + kThreads / 32 - 1) / (kThreads / 32));
-        rows_part_kernel<T, true><<<g1, kThreads, 0, s>>>(a);
+        rows_part_kernel<T, true, ACT, GATE><<<g1, kThreads, 0, s>>>(a);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        rows_bwd_kernel<T><<<dim3(p.blocks, a.N, (a.C + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);
+        rows_bwd_kernel<T, ACT, GATE><<<dim3(p.blocks, a.N, (a.C + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);
     }
     if ((e = cudaGetLastError()) != cudaSuccess || !a.dweight) return e;
     wsum_kernel<<<(2 * a.C + 31) / 32, 1024, 0, s>>>(a);
     return cudaGetLastError();
+}
+
+template <typename T, bool BWD>
+cudaError_t dispatch(const Args& a, const Plan& p, cudaStream_t s)
+{
+    auto go = [&](auto act, auto gate) {
+        constexpr int A = decltype(act)::value;
+        constexpr bool Z = decltype(gate)::value;
+        if constexpr (BWD) return bwd_typed<T, A, Z>(a, p, s);
+        else return fwd_typed<T, A, Z>(a, p, s);
+    };
+    using Silu = std::integral_constant<int, MDN_ACT_SILU>;
+    using None = std::integral_constant<int, MDN_ACT_NONE>;
+    if (a.act == MDN_ACT_SILU) return a.gate ? go(Silu{}, std::true_type{}) : go(Silu{}, std::false_type{});
+    return a.gate ? go(None{}, std::true_type{}) : go(None{}, std::false_type{});
 }
 
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -641,8 +961,8 @@ mdn_status mdn_group_norm_fwd(const void* x, const void* gate, mdn_dtype dtype, 
     a.part = static_cast<float*>(workspace);
     a.blocks = p.blocks;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = dtype == MDN_F32 ? gn::fwd_typed<float>(a, p, s)
-                                           : gn::fwd_typed<__nv_bfloat16>(a, p, s);
+    const cudaError_t e = dtype == MDN_F32 ? gn::dispatch<float, false>(a, p, s)
+                                           : gn::dispatch<__nv_bfloat16, false>(a, p, s);
     return e == cudaSuccess ? MDN_OK : cuda_fail(e);
 }
 
@@ -683,8 +1003,8 @@ mdn_status mdn_group_norm_bwd(const void* x, const void* gate, mdn_dtype dtype, 
     a.part = static_cast<float*>(workspace);
     a.wpart = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.part_bytes);
     a.blocks = p.blocks; a.prows = p.prows;
-    const cudaError_t e = dtype == MDN_F32 ? gn::bwd_typed<float>(a, p, s)
-                                           : gn::bwd_typed<__nv_bfloat16>(a, p, s);
+    const cudaError_t e = dtype == MDN_F32 ? gn::dispatch<float, true>(a, p, s)
+                                           : gn::dispatch<__nv_bfloat16, true>(a, p, s);
     return e == cudaSuccess ? MDN_OK : cuda_fail(e);
 }
 

@@ -24,22 +24,35 @@ from . import _lib
 from .api import _check, _dtype_code, _ptr, library
 
 
-@contextlib.contextmanager
-def _on(device: torch.device, stream: Optional[torch.cuda.Stream]):
-    """Makes ``device`` current and ``stream`` (if given) its current stream, so
-    that scratch is allocated, used and freed in that stream's order."""
-    if device.type != "cuda":
-        raise ValueError(f"tensors must be on a CUDA device, got {device}")
-    if stream is not None and stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
-    with torch.cuda.device(device), torch.cuda.stream(stream):
-        yield torch.cuda.current_stream(device).cuda_stream
+class _On:
+    """Makes ``device`` current and ``stream`` (if given) its current stream, so that
+    scratch is allocated, used and freed in that stream's order; gives the stream's
+    handle.  With no stream on the current device there is nothing to switch."""
+    __slots__ = ("device", "stream", "stack")
+
+    def __init__(self, device: torch.device, stream: Optional[torch.cuda.Stream]):
+        if device.type != "cuda":
+            raise ValueError(f"tensors must be on a CUDA device, got {device}")
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+        self.device, self.stream, self.stack = device, stream, None
+
+    def __enter__(self) -> int:
+        if self.stream is not None or self.device.index != torch.cuda.current_device():
+            self.stack = contextlib.ExitStack()
+            self.stack.enter_context(torch.cuda.device(self.device))
+            self.stack.enter_context(torch.cuda.stream(self.stream))
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
+
+    def __exit__(self, *exc):
+        if self.stack is not None:
+            self.stack.close()
 
 
 def _need(t, like, dtype, shape, name):
     if t is None:
         return
-    if (t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous()
+    if (t.dtype != dtype or t.shape != shape or not t.is_contiguous()
             or t.device != like.device):
         raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {like.device}, got "
                          f"{t.dtype} {tuple(t.shape)} contiguous={t.is_contiguous()} on {t.device}")
@@ -104,7 +117,7 @@ def _fwd(q, k, v, alpha_log, beta, scale, cu_seqlens, S0, C, out, want_vtilde, w
         _need(t, q, torch.float32, rows + (H,), name)
     _need(S0, q, torch.float32, (N, H, d, d), "S0")
     scale = _scale(scale, d)
-    with _on(q.device, stream) as s:
+    with _On(q.device, stream) as s:
         if out is None:
             # a packed buffer's rows behind the last sequence are not written
             new = torch.zeros_like if packed else torch.empty_like
@@ -176,7 +189,7 @@ def _bwd(q, k, alpha_log, beta, cu_seqlens, scale, vtilde, d_o, S0, dS_T, C, wor
     for name, t in (("S0", S0), ("dS_T", dS_T)):
         _need(t, q, torch.float32, (N, H, d, d), name)
     scale = _scale(scale, d)
-    with _on(q.device, stream) as s:
+    with _On(q.device, stream) as s:
         new = torch.zeros_like if packed else torch.empty_like
         g = dict(zip(_GRADS, (new(q), new(k), new(vtilde), new(alpha_log), new(beta),
                               torch.empty((N, H, d, d), dtype=torch.float32, device=q.device))))
@@ -237,7 +250,7 @@ def gdr_step(q, k, v, alpha_log, beta, scale: Optional[float], S: torch.Tensor, 
     for name, t in (("S", S), ("S_out", S_out)):
         _need(t, q, torch.float32, (B, H, d, d), name)
     scale = _scale(scale, d)
-    with _on(q.device, stream) as s:
+    with _On(q.device, stream) as s:
         o = torch.empty_like(v) if o is None else o
         if vtilde is None and want_vtilde:
             vtilde = torch.empty_like(v)

@@ -17,7 +17,7 @@ import torch
 
 from . import _lib
 from .api import _check, _dtype_code, _ptr, library
-from .gdr import _need, _on, _workspace
+from .gdr import _need, _On, _workspace
 
 _ACT = {"none": _lib.MDN_ACT_NONE, "silu": _lib.MDN_ACT_SILU}
 
@@ -53,7 +53,7 @@ def group_norm_fwd(x, groups: int, weight=None, bias=None, gate=None, eps: float
     """Returns (y, mean, rstd): y of x's shape and type, mean and rstd [N, groups]
     float32 (what :func:`group_norm_bwd` needs).  ``out`` may hold them preallocated."""
     N, L, C, code = _common(x, groups, weight, bias, gate, act)
-    with _on(x.device, stream) as s:
+    with _On(x.device, stream) as s:
         if out is None:
             st = lambda: torch.empty((N, groups), dtype=torch.float32, device=x.device)
             out = (torch.empty_like(x), st(), st())
@@ -78,7 +78,7 @@ def group_norm_bwd(x, groups: int, mean, rstd, dy, weight=None, bias=None, gate=
     _need(dy, x, x.dtype, x.shape, "dy")
     _need(mean, x, torch.float32, (N, groups), "mean")
     _need(rstd, x, torch.float32, (N, groups), "rstd")
-    with _on(x.device, stream) as s:
+    with _On(x.device, stream) as s:
         g = {"dx": torch.empty_like(x)}
         if gate is not None:
             g["dgate"] = torch.empty_like(x)

@@ -3,7 +3,7 @@
 //
 // The state is small (d x d) and its columns (rows, in the backward's last
 // kernel) do not depend on one another, so a chain keeps it in registers for
-// the whole sequence and walks the tokens.  A thread holds 4 columns and every
+// the whole sequence and walks the tokens.  A thread holds 1 or 4 columns and every
 // eighth float4 of rows; the 8 lanes that share a column reduce by shuffles.
 // One reduction per token is enough: with the state before the token,
 //     o_t = scale (alpha S^T q + beta (k.q) vtilde),
@@ -15,7 +15,8 @@ namespace mdn {
 namespace gdr {
 namespace {
 
-constexpr int TB = 16;   // tokens staged in shared memory at once
+constexpr int TB = 16;   // tokens staged in shared memory at once (two such buffers)
+constexpr int kGradTokens = 8;  // the same of the token gradients' kernel (more tensors a token)
 constexpr int RL = 8;    // lanes sharing a column (a row, in the token gradients)
 
 __device__ __forceinline__ float dot4(const float4 a, const float4 b, float c)
@@ -30,162 +31,259 @@ __device__ __forceinline__ float lanes_sum(float x)
     return x;
 }
 
-// n token rows of width W of a [rows, heads, D] tensor as fp32 into dst[.][W]
-// (zeros for tokens n .. TB-1); col0 is the first column.
-template <typename T, int W, int D, int NT_>
-__device__ __forceinline__ void stage(float (*dst)[W], const T* src, long long row0, int heads,
-                                      int head, int col0, int n)
+// n token rows of width W of a [rows, heads, D] tensor into dst[TB][W], as stored
+// and asynchronously, 16 bytes at a time (zeros for tokens n .. TB-1); col0 is the
+// first column.  Complete after stage_commit and stage_wait.
+template <typename T, int TB, int W, int D, int NT_>
+__device__ __forceinline__ void stage(T* dst, const T* src, long long row0, int heads, int head,
+                                      int col0, int n)
 {
-    for (int e = threadIdx.x; e < TB * W; e += NT_) {
-        const int t = e / W, c = e % W;
-        dst[t][c] = t < n ? ld_elem(src + ((size_t)(row0 + t) * heads + head) * D + col0 + c) : 0.f;
+    constexpr int P = W * (int)sizeof(T) / 16;  // pieces of a row
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    for (int e = threadIdx.x; e < TB * P; e += NT_) {
+        const int t = e / P, c = e % P;
+        const T* from = src + ((size_t)(row0 + (t < n ? t : 0)) * heads + head) * D + col0;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + e * 16),
+                     "l"(reinterpret_cast<const char*>(from) + c * 16), "r"(t < n ? 16 : 0)
+                     : "memory");
+    }
+}
+__device__ __forceinline__ void stage_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits for all but the newest group.
+__device__ __forceinline__ void stage_wait() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+
+__device__ __forceinline__ float4 get4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 get4(const __nv_bfloat16* p)
+{
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                       __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+}
+
+// Two buffers of TB token rows: `rows` elements of T (and `frows` floats) per token.
+template <typename T, int TB_, int ROWS>
+struct Buffers {
+    T* base;
+    __device__ __forceinline__ T* at(int k, int off) const { return base + ((size_t)(k & 1) * ROWS + off) * TB_; }
+};
+
+// Dot products of two staged rows, 8 lanes a token.
+template <typename T, int TB, int D, int NT_>
+__device__ __forceinline__ void dots(float* out, const T* x, const T* y, float f)
+{
+    for (int t = threadIdx.x / 8; t < TB; t += NT_ / 8) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = (threadIdx.x % 8) * 4; i < D; i += 32) s = dot4(get4(x + t * D + i), get4(y + t * D + i), s);
+        s = lanes_sum(s);
+        if (threadIdx.x % 8 == 0) out[t] = f * s;
     }
 }
 
-// ---------------------------------------------------------------- forward
-// One CTA: NC columns of one chain.
-template <typename T, int D, int NC>
-__global__ void __launch_bounds__(NC * 2) fwd_kernel(const Args a)
+// A thread's part of a state: CPT columns from c0, rows 4 rl .. of every 32.
+template <int D, int CPT>
+struct Part {
+    static constexpr int V = D / (4 * RL), R = 4 * V;  // rows of a thread
+    float s[R][CPT];
+    __device__ static __forceinline__ int row(int i, int rl) { return (i / 4) * (4 * RL) + rl * 4 + i % 4; }
+    __device__ __forceinline__ void load(const float* src, int rl)  // src: the first column, or null (zeros)
+    {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            if constexpr (CPT == 4) {
+                const float4 x = src ? *reinterpret_cast<const float4*>(src + (size_t)row(i, rl) * D)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+                s[i][0] = x.x; s[i][1] = x.y; s[i][2] = x.z; s[i][3] = x.w;
+            } else {
+#pragma unroll
+                for (int c = 0; c < CPT; ++c) s[i][c] = src ? src[(size_t)row(i, rl) * D + c] : 0.f;
+            }
+        }
+    }
+    __device__ __forceinline__ void store(float* dst, int rl) const
+    {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            if constexpr (CPT == 4) {
+                *reinterpret_cast<float4*>(dst + (size_t)row(i, rl) * D) =
+                    make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
+            } else {
+#pragma unroll
+                for (int c = 0; c < CPT; ++c) dst[(size_t)row(i, rl) * D + c] = s[i][c];
+            }
+        }
+    }
+};
+template <int V, typename T>
+__device__ __forceinline__ void get_rows(float (&x)[4 * V], const T* row, int rl)
 {
-    constexpr int NTH = NC * 2, V = D / (4 * RL);  // float4 rows groups per thread
-    __shared__ __align__(16) float ks[TB][D], qs[TB][D], vs[TB][NC];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const float4 k4 = get4(row + i * (4 * RL) + rl * 4);
+        x[4 * i] = k4.x; x[4 * i + 1] = k4.y; x[4 * i + 2] = k4.z; x[4 * i + 3] = k4.w;
+    }
+}
+template <int CPT, typename T>
+__device__ __forceinline__ void get_cols(float (&x)[CPT], const T* p)
+{
+    if constexpr (CPT == 4) {
+        const float4 v = get4(p);
+        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    } else {
+#pragma unroll
+        for (int c = 0; c < CPT; ++c) x[c] = ld_elem(p + c);
+    }
+}
+// x[rl], with x in registers.
+template <int CPT>
+__device__ __forceinline__ float pick(const float (&x)[CPT], int rl)
+{
+    float y = x[0];
+#pragma unroll
+    for (int c = 1; c < CPT; ++c) y = rl == c ? x[c] : y;
+    return y;
+}
+
+// ---------------------------------------------------------------- forward
+// One CTA: NC columns of one chain, CPT of them per thread.
+template <typename T, int D, int NC, int CPT>
+__global__ void __launch_bounds__(NC / CPT * RL) fwd_kernel(const Args a)
+{
+    constexpr int NTH = NC / CPT * RL, V = D / (4 * RL), R = 4 * V;
+    extern __shared__ __align__(16) uint8_t shm[];
+    const Buffers<T, TB, 2 * D + NC> buf{reinterpret_cast<T*>(shm)};  // k, q, v
     __shared__ float al[TB], be[TB], kq[TB];
     const Chain ch = chain_of(a, blockIdx.x / (D / NC));
     const int col0 = (blockIdx.x % (D / NC)) * NC;
-    const int tid = threadIdx.x, rl = tid % RL, cg = tid / RL;  // 4 columns 4 cg ..
-    float s[V * 4][4];
-    const size_t sbase = (size_t)ch.state * D * D + col0 + cg * 4;
-#pragma unroll
-    for (int i = 0; i < V * 4; ++i) {
-        const int r = (i / 4) * (4 * RL) + rl * 4 + i % 4;
-        const float4 x = a.S0 ? *reinterpret_cast<const float4*>(a.S0 + sbase + (size_t)r * D)
-                              : make_float4(0.f, 0.f, 0.f, 0.f);
-        s[i][0] = x.x; s[i][1] = x.y; s[i][2] = x.z; s[i][3] = x.w;
-    }
-    for (int t0 = 0; t0 < ch.len; t0 += TB) {
+    const int tid = threadIdx.x, rl = tid % RL, c0 = tid / RL * CPT;
+    const size_t sbase = (size_t)ch.state * D * D + col0 + c0;
+    Part<D, CPT> st;
+    st.load(a.S0 ? a.S0 + sbase : nullptr, rl);
+    float ga = 0.f, gb = 0.f;  // gates of token tid of the block being fetched
+    auto fetch = [&](int t0, int k) {
         const int n = min(TB, ch.len - t0);
         const long long row = ch.row0 + t0;
-        __syncthreads();
-        stage<T, D, D, NTH>(ks, static_cast<const T*>(a.k), row, a.Hk, ch.hk, 0, n);
-        stage<T, D, D, NTH>(qs, static_cast<const T*>(a.q), row, a.Hk, ch.hk, 0, n);
-        stage<T, NC, D, NTH>(vs, static_cast<const T*>(a.v), row, a.H, ch.h, col0, n);
-        if (tid < n) {
-            al[tid] = expf(a.alpha_log[(row + tid) * a.H + ch.h]);
-            be[tid] = a.beta[(row + tid) * a.H + ch.h];
-        }
-        __syncthreads();
-        for (int t = tid / 8; t < TB; t += NTH / 8) {  // k.q of each token, 8 lanes a token
-            float x = 0.f;
-            for (int i = tid % 8; i < D; i += 8) x = fmaf(ks[t][i], qs[t][i], x);
-            x = lanes_sum(x);
-            if (tid % 8 == 0) kq[t] = x;
-        }
-        __syncthreads();
-        for (int t = 0; t < n; ++t) {
-            float pk[4] = {0.f, 0.f, 0.f, 0.f}, pq[4] = {0.f, 0.f, 0.f, 0.f};
-            float kr[V * 4];
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float4 k4 = *reinterpret_cast<const float4*>(&ks[t][i * (4 * RL) + rl * 4]);
-                const float4 q4 = *reinterpret_cast<const float4*>(&qs[t][i * (4 * RL) + rl * 4]);
-                kr[4 * i] = k4.x; kr[4 * i + 1] = k4.y; kr[4 * i + 2] = k4.z; kr[4 * i + 3] = k4.w;
-                const float qr[4] = {q4.x, q4.y, q4.z, q4.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        pk[c] = fmaf(s[4 * i + e][c], kr[4 * i + e], pk[c]);
-                        pq[c] = fmaf(s[4 * i + e][c], qr[e], pq[c]);
-                    }
+        if (n > 0) {
+            stage<T, TB, D, D, NTH>(buf.at(k, 0), static_cast<const T*>(a.k), row, a.Hk, ch.hk, 0, n);
+            stage<T, TB, D, D, NTH>(buf.at(k, D), static_cast<const T*>(a.q), row, a.Hk, ch.hk, 0, n);
+            stage<T, TB, NC, D, NTH>(buf.at(k, 2 * D), static_cast<const T*>(a.v), row, a.H, ch.h, col0, n);
+            if (tid < n) {
+                ga = a.alpha_log[(row + tid) * a.H + ch.h];
+                gb = a.beta[(row + tid) * a.H + ch.h];
             }
-            const float alpha = al[t], b = be[t];
-            float x[4], ov[4];
+        }
+        stage_commit();
+    };
+    fetch(0, 0);
+    for (int t0 = 0, k = 0; t0 < ch.len; t0 += TB, ++k) {
+        const int n = min(TB, ch.len - t0);
+        const T* ks = buf.at(k, 0);
+        const T* qs = buf.at(k, D);
+        const T* vs = buf.at(k, 2 * D);
+        __syncthreads();  // the other buffer, al, be, kq are free
+        if (tid < TB) {
+            al[tid] = expf(ga);
+            be[tid] = gb;
+        }
+        fetch(t0 + TB, k + 1);
+        stage_wait();
+        __syncthreads();
+        dots<T, TB, D, NTH>(kq, ks, qs, 1.f);
+        __syncthreads();
+        const size_t out0 = ((size_t)(ch.row0 + t0) * a.H + ch.h) * D + col0 + c0;
+        // lane c of a column group stores o of its column c, lane CPT + c vtilde
+        T* dst = rl < CPT ? static_cast<T*>(a.o) + out0 + rl
+                          : a.vt && rl < 2 * CPT ? static_cast<T*>(a.vt) + out0 + rl - CPT : nullptr;
+#pragma unroll 2
+        for (int t = 0; t < n; ++t) {
+            float pk[CPT], pq[CPT], kr[R], qr[R], v[CPT];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                x[c] = vs[t][cg * 4 + c] - alpha * lanes_sum(pk[c]);
+            for (int c = 0; c < CPT; ++c) pk[c] = pq[c] = 0.f;
+            get_rows<V>(kr, ks + t * D, rl);
+            get_rows<V>(qr, qs + t * D, rl);
+            get_cols<CPT>(v, vs + t * NC + c0);
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int c = 0; c < CPT; ++c) {
+                    pk[c] = fmaf(st.s[i][c], kr[i], pk[c]);
+                    pq[c] = fmaf(st.s[i][c], qr[i], pq[c]);
+                }
+            const float alpha = al[t], b = be[t];
+            float x[CPT], ov[CPT];
+#pragma unroll
+            for (int c = 0; c < CPT; ++c) {
+                x[c] = v[c] - alpha * lanes_sum(pk[c]);
                 ov[c] = a.scale * fmaf(alpha, lanes_sum(pq[c]), b * kq[t] * x[c]);
             }
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < CPT; ++c) {
                 const float bx = b * x[c];
 #pragma unroll
-                for (int i = 0; i < V * 4; ++i) s[i][c] = fmaf(alpha, s[i][c], kr[i] * bx);
+                for (int i = 0; i < R; ++i) st.s[i][c] = fmaf(alpha, st.s[i][c], kr[i] * bx);
             }
-            const size_t out = ((size_t)(row + t) * a.H + ch.h) * D + col0 + cg * 4;
-            if (rl < 4) {
-                float y = ov[0];
-                y = rl == 1 ? ov[1] : rl == 2 ? ov[2] : rl == 3 ? ov[3] : y;
-                st_elem(static_cast<T*>(a.o) + out + rl, y);
-            } else if (a.vt) {
-                float y = x[0];
-                y = rl == 5 ? x[1] : rl == 6 ? x[2] : rl == 7 ? x[3] : y;
-                st_elem(static_cast<T*>(a.vt) + out + rl - 4, y);
-            }
+            if (dst) st_elem(dst + (size_t)t * a.H * D, rl < CPT ? pick<CPT>(ov, rl) : pick<CPT>(x, rl - CPT));
         }
     }
-#pragma unroll
-    for (int i = 0; i < V * 4; ++i) {
-        const int r = (i / 4) * (4 * RL) + rl * 4 + i % 4;
-        *reinterpret_cast<float4*>(a.S_T + sbase + (size_t)r * D) =
-            make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
-    }
+    st.store(a.S_T + sbase, rl);
 }
 
 // ---------------------------------------------------------------- backward
 // S entering each chunk, from the saved vtilde (no chain of products: the
 // update of a token reads nothing of the state but its scale).
-template <typename T, int D, int NC>
-__global__ void __launch_bounds__(NC * 2) states_kernel(const Args a)
+template <typename T, int D, int NC, int CPT>
+__global__ void __launch_bounds__(NC / CPT * RL) states_kernel(const Args a)
 {
-    constexpr int NTH = NC * 2, V = D / (4 * RL);
-    __shared__ __align__(16) float ks[TB][D], vs[TB][NC];
+    constexpr int NTH = NC / CPT * RL, V = D / (4 * RL), R = 4 * V;
+    extern __shared__ __align__(16) uint8_t shm[];
+    const Buffers<T, TB, D + NC> buf{reinterpret_cast<T*>(shm)};  // k, vtilde
     __shared__ float al[TB], be[TB];
     const Chain ch = chain_of(a, blockIdx.x / (D / NC));
     const int col0 = (blockIdx.x % (D / NC)) * NC;
-    const int tid = threadIdx.x, rl = tid % RL, cg = tid / RL;
-    float s[V * 4][4];
-    const size_t sbase = (size_t)ch.state * D * D + col0 + cg * 4;
-#pragma unroll
-    for (int i = 0; i < V * 4; ++i) {
-        const int r = (i / 4) * (4 * RL) + rl * 4 + i % 4;
-        const float4 x = a.S0 ? *reinterpret_cast<const float4*>(a.S0 + sbase + (size_t)r * D)
-                              : make_float4(0.f, 0.f, 0.f, 0.f);
-        s[i][0] = x.x; s[i][1] = x.y; s[i][2] = x.z; s[i][3] = x.w;
-    }
-    for (int t0 = 0; t0 < ch.len; t0 += TB) {
-        if (t0 % kChunk == 0) {
-            float* dst = a.SS + ((size_t)(ch.chunk0 + t0 / kChunk) * a.H + ch.h) * D * D + col0 + cg * 4;
-#pragma unroll
-            for (int i = 0; i < V * 4; ++i) {
-                const int r = (i / 4) * (4 * RL) + rl * 4 + i % 4;
-                *reinterpret_cast<float4*>(dst + (size_t)r * D) =
-                    make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
-            }
-        }
+    const int tid = threadIdx.x, rl = tid % RL, c0 = tid / RL * CPT;
+    const size_t sbase = (size_t)ch.state * D * D + col0 + c0;
+    Part<D, CPT> st;
+    st.load(a.S0 ? a.S0 + sbase : nullptr, rl);
+    float ga = 0.f, gb = 0.f;
+    auto fetch = [&](int t0, int k) {
         const int n = min(TB, ch.len - t0);
         const long long row = ch.row0 + t0;
-        __syncthreads();
-        stage<T, D, D, NTH>(ks, static_cast<const T*>(a.k), row, a.Hk, ch.hk, 0, n);
-        stage<T, NC, D, NTH>(vs, static_cast<const T*>(a.vt), row, a.H, ch.h, col0, n);
-        if (tid < n) {
-            al[tid] = expf(a.alpha_log[(row + tid) * a.H + ch.h]);
-            be[tid] = a.beta[(row + tid) * a.H + ch.h];
+        if (n > 0) {
+            stage<T, TB, D, D, NTH>(buf.at(k, 0), static_cast<const T*>(a.k), row, a.Hk, ch.hk, 0, n);
+            stage<T, TB, NC, D, NTH>(buf.at(k, D), static_cast<const T*>(a.vt), row, a.H, ch.h, col0, n);
+            if (tid < n) {
+                ga = a.alpha_log[(row + tid) * a.H + ch.h];
+                gb = a.beta[(row + tid) * a.H + ch.h];
+            }
         }
+        stage_commit();
+    };
+    fetch(0, 0);
+    for (int t0 = 0, k = 0; t0 < ch.len; t0 += TB, ++k) {
+        if (t0 % kChunk == 0)
+            st.store(a.SS + ((size_t)(ch.chunk0 + t0 / kChunk) * a.H + ch.h) * D * D + col0 + c0, rl);
+        const int n = min(TB, ch.len - t0);
+        const T* ks = buf.at(k, 0);
+        const T* vs = buf.at(k, D);
         __syncthreads();
+        if (tid < TB) {
+            al[tid] = expf(ga);
+            be[tid] = gb;
+        }
+        fetch(t0 + TB, k + 1);
+        stage_wait();
+        __syncthreads();
+#pragma unroll 4
         for (int t = 0; t < n; ++t) {
-            const float alpha = al[t];
-            float bx[4];
+            const float alpha = al[t], b = be[t];
+            float kr[R], v[CPT];
+            get_rows<V>(kr, ks + t * D, rl);
+            get_cols<CPT>(v, vs + t * NC + c0);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) bx[c] = be[t] * vs[t][cg * 4 + c];
+            for (int c = 0; c < CPT; ++c) {
+                const float bx = b * v[c];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float4 k4 = *reinterpret_cast<const float4*>(&ks[t][i * (4 * RL) + rl * 4]);
-                const float kr[4] = {k4.x, k4.y, k4.z, k4.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        s[4 * i + e][c] = fmaf(alpha, s[4 * i + e][c], kr[e] * bx[c]);
+                for (int i = 0; i < R; ++i) st.s[i][c] = fmaf(alpha, st.s[i][c], kr[i] * bx);
             }
         }
     }
@@ -194,98 +292,84 @@ __global__ void __launch_bounds__(NC * 2) states_kernel(const Args a)
 // The reverse chain: dv, the adjoint of S leaving each chunk, dS0.  As in the
 // forward pass one reduction per token: with the adjoint G' from the later
 // tokens, dv = beta (G'^T k + scale (q.k) do).
-template <typename T, int D, int NC>
-__global__ void __launch_bounds__(NC * 2) reverse_kernel(const Args a)
+template <typename T, int D, int NC, int CPT>
+__global__ void __launch_bounds__(NC / CPT * RL) reverse_kernel(const Args a)
 {
-    constexpr int NTH = NC * 2, V = D / (4 * RL);
-    __shared__ __align__(16) float ks[TB][D], qs[TB][D], os[TB][NC];
+    constexpr int NTH = NC / CPT * RL, V = D / (4 * RL), R = 4 * V;
+    extern __shared__ __align__(16) uint8_t shm[];
+    const Buffers<T, TB, 2 * D + NC> buf{reinterpret_cast<T*>(shm)};  // k, q, do
     __shared__ float al[TB], be[TB], kq[TB];
     const Chain ch = chain_of(a, blockIdx.x / (D / NC));
     const int col0 = (blockIdx.x % (D / NC)) * NC;
-    const int tid = threadIdx.x, rl = tid % RL, cg = tid / RL;
-    float g[V * 4][4];
-    const size_t sbase = (size_t)ch.state * D * D + col0 + cg * 4;
-#pragma unroll
-    for (int i = 0; i < V * 4; ++i) {
-        const int r = (i / 4) * (4 * RL) + rl * 4 + i % 4;
-        const float4 x = a.dS_T ? *reinterpret_cast<const float4*>(a.dS_T + sbase + (size_t)r * D)
-                                : make_float4(0.f, 0.f, 0.f, 0.f);
-        g[i][0] = x.x; g[i][1] = x.y; g[i][2] = x.z; g[i][3] = x.w;
-    }
-    for (int t0 = (ch.len - 1) / TB * TB; t0 >= 0 && ch.len > 0; t0 -= TB) {
+    const int tid = threadIdx.x, rl = tid % RL, c0 = tid / RL * CPT;
+    const size_t sbase = (size_t)ch.state * D * D + col0 + c0;
+    Part<D, CPT> g;
+    g.load(a.dS_T ? a.dS_T + sbase : nullptr, rl);
+    float ga = 0.f, gb = 0.f;
+    auto fetch = [&](int t0, int k) {
+        if (t0 >= 0) {
+            const int n = min(TB, ch.len - t0);
+            const long long row = ch.row0 + t0;
+            stage<T, TB, D, D, NTH>(buf.at(k, 0), static_cast<const T*>(a.k), row, a.Hk, ch.hk, 0, n);
+            stage<T, TB, D, D, NTH>(buf.at(k, D), static_cast<const T*>(a.q), row, a.Hk, ch.hk, 0, n);
+            stage<T, TB, NC, D, NTH>(buf.at(k, 2 * D), static_cast<const T*>(a.d_o), row, a.H, ch.h, col0, n);
+            if (tid < n) {
+                ga = a.alpha_log[(row + tid) * a.H + ch.h];
+                gb = a.beta[(row + tid) * a.H + ch.h];
+            }
+        }
+        stage_commit();
+    };
+    const int top = ch.len > 0 ? (ch.len - 1) / TB * TB : -TB;
+    fetch(top, 0);
+    for (int t0 = top, k = 0; t0 >= 0; t0 -= TB, ++k) {
         const int n = min(TB, ch.len - t0);
-        if (t0 + n == ch.len || (t0 + TB) % kChunk == 0) {
-            float* dst = a.GG + ((size_t)(ch.chunk0 + t0 / kChunk) * a.H + ch.h) * D * D + col0 + cg * 4;
-#pragma unroll
-            for (int i = 0; i < V * 4; ++i) {
-                const int r = (i / 4) * (4 * RL) + rl * 4 + i % 4;
-                *reinterpret_cast<float4*>(dst + (size_t)r * D) =
-                    make_float4(g[i][0], g[i][1], g[i][2], g[i][3]);
-            }
-        }
-        const long long row = ch.row0 + t0;
+        if (t0 + n == ch.len || (t0 + TB) % kChunk == 0)
+            g.store(a.GG + ((size_t)(ch.chunk0 + t0 / kChunk) * a.H + ch.h) * D * D + col0 + c0, rl);
+        const T* ks = buf.at(k, 0);
+        const T* qs = buf.at(k, D);
+        const T* os = buf.at(k, 2 * D);
         __syncthreads();
-        stage<T, D, D, NTH>(ks, static_cast<const T*>(a.k), row, a.Hk, ch.hk, 0, n);
-        stage<T, D, D, NTH>(qs, static_cast<const T*>(a.q), row, a.Hk, ch.hk, 0, n);
-        stage<T, NC, D, NTH>(os, static_cast<const T*>(a.d_o), row, a.H, ch.h, col0, n);
-        if (tid < n) {
-            al[tid] = expf(a.alpha_log[(row + tid) * a.H + ch.h]);
-            be[tid] = a.beta[(row + tid) * a.H + ch.h];
+        if (tid < TB) {
+            al[tid] = expf(ga);
+            be[tid] = gb;
         }
+        fetch(t0 - TB, k + 1);
+        stage_wait();
         __syncthreads();
-        for (int t = tid / 8; t < TB; t += NTH / 8) {
-            float x = 0.f;
-            for (int i = tid % 8; i < D; i += 8) x = fmaf(ks[t][i], qs[t][i], x);
-            x = lanes_sum(x);
-            if (tid % 8 == 0) kq[t] = a.scale * x;
-        }
+        dots<T, TB, D, NTH>(kq, ks, qs, a.scale);
         __syncthreads();
+        const size_t out0 = ((size_t)(ch.row0 + t0) * a.H + ch.h) * D + col0 + c0 + rl;
+#pragma unroll 2
         for (int t = n - 1; t >= 0; --t) {
-            float p[4] = {0.f, 0.f, 0.f, 0.f};
-            float kr[V * 4];
+            float p[CPT], kr[R], qr[R], o[CPT];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float4 k4 = *reinterpret_cast<const float4*>(&ks[t][i * (4 * RL) + rl * 4]);
-                kr[4 * i] = k4.x; kr[4 * i + 1] = k4.y; kr[4 * i + 2] = k4.z; kr[4 * i + 3] = k4.w;
+            for (int c = 0; c < CPT; ++c) p[c] = 0.f;
+            get_rows<V>(kr, ks + t * D, rl);
+            get_rows<V>(qr, qs + t * D, rl);
+            get_cols<CPT>(o, os + t * NC + c0);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
+            for (int i = 0; i < R; ++i)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) p[c] = fmaf(g[4 * i + e][c], kr[4 * i + e], p[c]);
-            }
+                for (int c = 0; c < CPT; ++c) p[c] = fmaf(g.s[i][c], kr[i], p[c]);
             const float alpha = al[t];
-            float dv[4], od[4];
+            float dv[CPT];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float d = os[t][cg * 4 + c];
-                dv[c] = be[t] * fmaf(kq[t], d, lanes_sum(p[c]));
-                od[c] = a.scale * d;
+            for (int c = 0; c < CPT; ++c) {
+                const float od = a.scale * o[c];
+                dv[c] = be[t] * fmaf(kq[t], o[c], lanes_sum(p[c]));
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+                    g.s[i][c] = alpha * fmaf(-kr[i], dv[c], fmaf(qr[i], od, g.s[i][c]));
             }
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float4 q4 = *reinterpret_cast<const float4*>(&qs[t][i * (4 * RL) + rl * 4]);
-                const float qr[4] = {q4.x, q4.y, q4.z, q4.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        g[4 * i + e][c] = alpha * fmaf(-kr[4 * i + e], dv[c],
-                                                       fmaf(qr[e], od[c], g[4 * i + e][c]));
-            }
-            if (rl < 4) {
-                float y = dv[0];
-                y = rl == 1 ? dv[1] : rl == 2 ? dv[2] : rl == 3 ? dv[3] : y;
-                const size_t out = ((size_t)(row + t) * a.H + ch.h) * D + col0 + cg * 4 + rl;
-                a.dvf[out] = y;
-                st_elem(static_cast<T*>(a.dv) + out, y);
+            if (rl < CPT) {
+                const float y = pick<CPT>(dv, rl);
+                a.dvf[out0 + (size_t)t * a.H * D] = y;
+                st_elem(static_cast<T*>(a.dv) + out0 + (size_t)t * a.H * D, y);
             }
         }
     }
-#pragma unroll
-    for (int i = 0; i < V * 4; ++i) {
-        const int r = (i / 4) * (4 * RL) + rl * 4 + i % 4;
-        *reinterpret_cast<float4*>(a.dS0 + sbase + (size_t)r * D) =
-            make_float4(g[i][0], g[i][1], g[i][2], g[i][3]);
-    }
+    g.store(a.dS0 + sbase, rl);
 }
 
 // The token gradients of one chunk of one head, from the S entering it and
@@ -297,14 +381,11 @@ __global__ void __launch_bounds__(NC * 2) reverse_kernel(const Args a)
 template <typename T, int D>
 __global__ void __launch_bounds__(D * 2) token_grads_kernel(const Args a)
 {
-    constexpr int NTH = D * 2, V = D / (4 * RL), NW = NTH / 32;
-    extern __shared__ __align__(16) float sh[];
-    float (*c0)[D] = reinterpret_cast<float (*)[D]>(sh);               // do (forward), vtilde
-    float (*c1)[D] = reinterpret_cast<float (*)[D]>(sh + TB * D);      // dv
-    float (*c2)[D] = reinterpret_cast<float (*)[D]>(sh + 2 * TB * D);  // vtilde (forward), do
-    float (*ks)[D] = reinterpret_cast<float (*)[D]>(sh + 3 * TB * D);
-    float (*qs)[D] = reinterpret_cast<float (*)[D]>(sh + 4 * TB * D);
-    float (*dks)[D] = reinterpret_cast<float (*)[D]>(sh + 5 * TB * D);  // [64] alpha S dv
+    constexpr int NTH = D * 2, V = D / (4 * RL), NW = NTH / 32, TB = kGradTokens;
+    extern __shared__ __align__(16) uint8_t shm[];
+    float (*dks)[D] = reinterpret_cast<float (*)[D]>(shm);       // [64] alpha S dv
+    const Buffers<float, TB, D> fbuf{reinterpret_cast<float*>(shm + kChunk * D * 4)};  // dv
+    const Buffers<T, TB, 4 * D> buf{reinterpret_cast<T*>(shm + (kChunk + 2 * TB) * D * 4)};  // do, vtilde, k, q
     __shared__ float al[TB], be[TB], dd[TB];
     __shared__ float cc[kChunk][NW], bb[kChunk][NW];  // a warp's share of q.dq - k.(alpha S dv); dbeta
     __shared__ float ip[NW];
@@ -325,45 +406,58 @@ __global__ void __launch_bounds__(D * 2) token_grads_kernel(const Args a)
                 s[r][4 * i] = x.x; s[r][4 * i + 1] = x.y; s[r][4 * i + 2] = x.z; s[r][4 * i + 3] = x.w;
             }
     };
-    auto stage_all = [&](int t0, int m, const T* x0, const T* x2) {
+    // blocks of tokens: forward over the chunk, then backward; k counts them
+    float ga = 0.f, gb = 0.f;
+    auto fetch = [&](int t0, int k) {
+        const int m = min(TB, cr.valid - t0);
         const long long row = cr.row0 + t0;
-        __syncthreads();
-        stage<T, D, D, NTH>(c0, x0, row, a.H, h, 0, m);
-        stage<float, D, D, NTH>(c1, a.dvf, row, a.H, h, 0, m);
-        stage<T, D, D, NTH>(c2, x2, row, a.H, h, 0, m);
-        stage<T, D, D, NTH>(ks, static_cast<const T*>(a.k), row, a.Hk, hk, 0, m);
-        stage<T, D, D, NTH>(qs, static_cast<const T*>(a.q), row, a.Hk, hk, 0, m);
-        if (tid < m) {
-            al[tid] = expf(a.alpha_log[(row + tid) * a.H + h]);
-            be[tid] = a.beta[(row + tid) * a.H + h];
+        if (t0 >= 0 && m > 0) {
+            stage<float, TB, D, D, NTH>(fbuf.at(k, 0), a.dvf, row, a.H, h, 0, m);
+            stage<T, TB, D, D, NTH>(buf.at(k, 0), static_cast<const T*>(a.d_o), row, a.H, h, 0, m);
+            stage<T, TB, D, D, NTH>(buf.at(k, D), static_cast<const T*>(a.vt), row, a.H, h, 0, m);
+            stage<T, TB, D, D, NTH>(buf.at(k, 2 * D), static_cast<const T*>(a.k), row, a.Hk, hk, 0, m);
+            stage<T, TB, D, D, NTH>(buf.at(k, 3 * D), static_cast<const T*>(a.q), row, a.Hk, hk, 0, m);
+            if (tid < m) {
+                ga = a.alpha_log[(row + tid) * a.H + h];
+                gb = a.beta[(row + tid) * a.H + h];
+            }
         }
+        stage_commit();
+    };
+    auto turn = [&](int next, int k) {  // block k has landed, block k + 1 is on its way
         __syncthreads();
-        for (int t = tid / 8; t < TB; t += NTH / 8) {
-            float x = 0.f;
-            for (int i = tid % 8; i < D; i += 8) x = fmaf(c0[t][i], c2[t][i], x);
-            x = lanes_sum(x);
-            if (tid % 8 == 0) dd[t] = x;  // do . vtilde
+        if (tid < TB) {
+            al[tid] = expf(ga);
+            be[tid] = gb;
         }
+        fetch(next, k + 1);
+        stage_wait();
+        __syncthreads();
+        dots<T, TB, D, NTH>(dd, buf.at(k, 0), buf.at(k, D), 1.f);  // do . vtilde
         __syncthreads();
     };
-    const T* vt = static_cast<const T*>(a.vt);
-    const T* dout = static_cast<const T*>(a.d_o);
+    const int top = (cr.valid - 1) / TB * TB;
+    int blk = 0;
+    fetch(0, 0);
     load(a.SS);
-    for (int t0 = 0; t0 < cr.valid; t0 += TB) {
+    for (int t0 = 0; t0 < cr.valid; t0 += TB, ++blk) {
         const int m = min(TB, cr.valid - t0);
-        stage_all(t0, m, dout, vt);
+        turn(t0 + TB < cr.valid ? t0 + TB : top, blk);
+        const float* c1 = fbuf.at(blk, 0);
+        const T* c0 = buf.at(blk, 0);
+        const T* c2 = buf.at(blk, D);
+        const T* ks = buf.at(blk, 2 * D);
+        const T* qs = buf.at(blk, 3 * D);
         for (int t = 0; t < m; ++t) {
             float po[4] = {0.f, 0.f, 0.f, 0.f}, pd[4] = {0.f, 0.f, 0.f, 0.f};
             const float alpha = al[t], b = be[t];
-            float bk[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) bk[r] = b * ks[t][row4 + r];
+            const float4 k4 = get4(ks + t * D + row4), q4 = get4(qs + t * D + row4);
+            const float kr[4] = {k4.x, k4.y, k4.z, k4.w}, qr[4] = {q4.x, q4.y, q4.z, q4.w};
+            const float bk[4] = {b * k4.x, b * k4.y, b * k4.z, b * k4.w};
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int c = i * (4 * RL) + rl * 4;
-                const float4 o4 = *reinterpret_cast<const float4*>(&c0[t][c]);
-                const float4 d4 = *reinterpret_cast<const float4*>(&c1[t][c]);
-                const float4 v4 = *reinterpret_cast<const float4*>(&c2[t][c]);
+                const float4 o4 = get4(c0 + t * D + c), d4 = get4(c1 + t * D + c), v4 = get4(c2 + t * D + c);
                 const float vv[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
@@ -381,7 +475,7 @@ __global__ void __launch_bounds__(D * 2) token_grads_kernel(const Args a)
             for (int r = 0; r < 4; ++r) {
                 dq[r] = a.scale * fmaf(alpha, lanes_sum(po[r]), bk[r] * dd[t]);
                 pd[r] = alpha * lanes_sum(pd[r]);
-                share += qs[t][row4 + r] * dq[r] - ks[t][row4 + r] * pd[r];
+                share += qr[r] * dq[r] - kr[r] * pd[r];
             }
             const size_t tok = (size_t)(cr.row0 + t0 + t);
             if (rl < 4) {
@@ -413,24 +507,24 @@ __global__ void __launch_bounds__(D * 2) token_grads_kernel(const Args a)
         if (lane == 0) ip[warp] = x;
     }
     load(a.GG);
-    for (int t0 = (cr.valid - 1) / TB * TB; t0 >= 0; t0 -= TB) {
+    for (int t0 = top; t0 >= 0; t0 -= TB, ++blk) {
         const int m = min(TB, cr.valid - t0);
-        stage_all(t0, m, vt, dout);
+        turn(t0 - TB, blk);
+        const float* c1 = fbuf.at(blk, 0);
+        const T* c2 = buf.at(blk, 0);
+        const T* c0 = buf.at(blk, D);
+        const T* ks = buf.at(blk, 2 * D);
+        const T* qs = buf.at(blk, 3 * D);
         for (int t = m - 1; t >= 0; --t) {
             float p[4] = {0.f, 0.f, 0.f, 0.f};
             const float alpha = al[t], b = be[t];
-            float sq[4], kr[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                sq[r] = a.scale * qs[t][row4 + r];
-                kr[r] = ks[t][row4 + r];
-            }
+            const float4 k4 = get4(ks + t * D + row4), q4 = get4(qs + t * D + row4);
+            const float kr[4] = {k4.x, k4.y, k4.z, k4.w};
+            const float sq[4] = {a.scale * q4.x, a.scale * q4.y, a.scale * q4.z, a.scale * q4.w};
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int c = i * (4 * RL) + rl * 4;
-                const float4 v4 = *reinterpret_cast<const float4*>(&c0[t][c]);
-                const float4 d4 = *reinterpret_cast<const float4*>(&c1[t][c]);
-                const float4 o4 = *reinterpret_cast<const float4*>(&c2[t][c]);
+                const float4 v4 = get4(c0 + t * D + c), d4 = get4(c1 + t * D + c), o4 = get4(c2 + t * D + c);
                 const float vv[4] = {v4.x, v4.y, v4.z, v4.w}, dv[4] = {d4.x, d4.y, d4.z, d4.w};
                 const float od[4] = {o4.x, o4.y, o4.z, o4.w};
 #pragma unroll
@@ -531,48 +625,54 @@ int sm_count()
     return sms;
 }
 
-// Columns per CTA: 32 while the narrow CTAs fit on the SMs four at a time
-// (the shortest walk per token), else the whole head (a token's q and k are
-// then staged once).
+// One kernel with its dynamic shared memory.
+template <typename K>
+cudaError_t run(K kernel, long long blocks, int threads, size_t shm, cudaStream_t s, const Args& a)
+{
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shm);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)blocks, threads, shm, s>>>(a);
+    return cudaGetLastError();
+}
+
+// Columns per CTA and thread.  Few chains: 32 columns a CTA and one a thread, so
+// that a token costs a warp few instructions (with one warp per scheduler each
+// takes five to six cycles, whatever it does: four columns a thread took 0.94 us a
+// token at d = 64, one 0.20 us); while those CTAs are at most two per SM.  More: the whole head a CTA and
+// four columns a thread, which reads each staged k and q once for four columns.
 template <typename T, int D>
 cudaError_t fwd_typed(const Args& a, cudaStream_t s)
 {
     const long long n = chains(a);
     ProfScope ps(kGdrFwdSimt, s);
-    if (n * (D / 32) <= 4LL * sm_count())
-        fwd_kernel<T, D, 32><<<(unsigned)(n * (D / 32)), 64, 0, s>>>(a);
-    else
-        fwd_kernel<T, D, D><<<(unsigned)n, 2 * D, 0, s>>>(a);
-    return cudaGetLastError();
+    if (n * (D / 32) <= 2LL * sm_count())
+        return run(fwd_kernel<T, D, 32, 1>, n * (D / 32), 32 * RL, 2 * TB * (2 * D + 32) * sizeof(T), s, a);
+    return run(fwd_kernel<T, D, D, 4>, n, 2 * D, 2 * TB * 3 * D * sizeof(T), s, a);
 }
 
 template <typename T, int D>
 cudaError_t bwd_typed(const Args& a, cudaStream_t s)
 {
     const long long n = chains(a);
-    const bool narrow = n * (D / 32) <= 4LL * sm_count();
+    const bool narrow = n * (D / 32) <= 2LL * sm_count();
     cudaError_t e;
     {
         ProfScope ps(kGdrBwdStates, s);
-        if (narrow) states_kernel<T, D, 32><<<(unsigned)(n * (D / 32)), 64, 0, s>>>(a);
-        else states_kernel<T, D, D><<<(unsigned)n, 2 * D, 0, s>>>(a);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        e = narrow ? run(states_kernel<T, D, 32, 1>, n * (D / 32), 32 * RL, 2 * TB * (D + 32) * sizeof(T), s, a)
+                   : run(states_kernel<T, D, D, 4>, n, 2 * D, 2 * TB * 2 * D * sizeof(T), s, a);
+        if (e != cudaSuccess) return e;
     }
     {
         ProfScope ps(kGdrBwdChain, s);
-        if (narrow) reverse_kernel<T, D, 32><<<(unsigned)(n * (D / 32)), 64, 0, s>>>(a);
-        else reverse_kernel<T, D, D><<<(unsigned)n, 2 * D, 0, s>>>(a);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        e = narrow ? run(reverse_kernel<T, D, 32, 1>, n * (D / 32), 32 * RL, 2 * TB * (2 * D + 32) * sizeof(T), s, a)
+                   : run(reverse_kernel<T, D, D, 4>, n, 2 * D, 2 * TB * 3 * D * sizeof(T), s, a);
+        if (e != cudaSuccess) return e;
     }
-    constexpr int shm = (5 * TB + kChunk) * D * (int)sizeof(float);
-    if ((e = cudaFuncSetAttribute(token_grads_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  shm)) != cudaSuccess)
-        return e;
     const long long blocks = chunks(a) * a.H;
     if (blocks == 0) return cudaSuccess;
     ProfScope ps(kGdrBwdGrads, s);
-    token_grads_kernel<T, D><<<(unsigned)blocks, 2 * D, shm, s>>>(a);
-    return cudaGetLastError();
+    return run(token_grads_kernel<T, D>, blocks, 2 * D,
+               (kChunk + 2 * kGradTokens) * D * sizeof(float) + 2 * kGradTokens * 4 * D * sizeof(T), s, a);
 }
 
 }  // namespace

@@ -19,9 +19,11 @@
 // bf16 terms.  The gate gradients are fp32: their products P1, P2 and [K; Q] K^T have
 // exact bf16 factors, dv in two terms.  P1 = dO Vtilde^T, P2 = dv Vtilde^T.
 //
-// One CTA of 256 threads per SM (176 KB of operands), bound by the latency of its
-// phases: loads, [K; Q] K^T and the P products, the rows of M (warps 0..3) beside the
-// scaling of dO, Vtilde and dv in place (warps 4..7), the products, the stores.
+// One CTA per SM (176 KB of operands), bound by the latency of its phases: loads,
+// [K; Q] K^T and the P products, the rows of M (twelve warps, a 32 x 16 block each) and the
+// scaling of dO, Vtilde and dv in place, the products, the stores.  A scheduler with one
+// warp issues every fifth cycle at best, so the phases' work is spread over 16 warps (on 8
+// warps the kernel took 113 us at the 400M layer's shape).
 #include "gdr_tc.cuh"
 
 namespace mdn {
@@ -32,7 +34,7 @@ using namespace sm100;
 using namespace tc;
 using inter::wait_bar;
 
-constexpr int D = 128, kThreads = 256;
+constexpr int D = 128, kThreads = 512;
 constexpr uint32_t KQ = 0;               // [K; Q]: 2 panels of 128 rows
 constexpr uint32_t DV = 32768;           // [dv; dO]: the same
 constexpr uint32_t VT = 65536;           // Vtilde: 2 panels of 64 rows
@@ -43,8 +45,10 @@ constexpr uint32_t M1 = GB + 32768;      // M1, -M2: 64 rows x 128 B
 constexpr uint32_t M2 = M1 + 8192;
 constexpr uint32_t VEC = M2 + 8192;      // gate vectors
 constexpr uint32_t REC = VEC + 1024;     // the chunk's record
-constexpr uint32_t CS = REC + kBwdRecBytes;  // sums of Z: [2][64] rows, [4][64] columns by warp
-constexpr uint32_t BT = CS + 6 * 256;    // [4] block factors
+constexpr uint32_t CS = REC + kBwdRecBytes;  // sums of Z by the warps that formed them: [4][128] of rows
+constexpr int kCsCols = 512;             // (lanes 0..63 of M2, 64..127 of M1), [4][64] of columns
+constexpr uint32_t GS = CS + (512 + 256) * 4;  // [4][64] sums of po, px, pb, pw over the slices; [256]: of gs
+constexpr uint32_t BT = GS + 4 * 256 + 16;   // [4] block factors
 constexpr uint32_t BARS = BT + 16;
 constexpr uint32_t MISC = BARS + 48;
 constexpr uint32_t BYTES = MISC + 16;
@@ -126,6 +130,53 @@ grads_kernel(const __grid_constant__ GradMaps tm, const Args a)
     float* bt = reinterpret_cast<float*>(sm + BT);
     float* rec = reinterpret_cast<float*>(sm + REC);
     float* cs = reinterpret_cast<float*>(sm + CS);
+    float* rows = cs;
+    float* gs = reinterpret_cast<float*>(sm + GS);
+    // gate vectors, record and the chains' sums of a head: warps 8 .. 14, under the loads
+    auto head_scalars = [&](int h) {
+        if (warp == 8) {
+            float ga[2], gb[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int t = 2 * lane + e;
+                const bool in = t < cr.valid;
+                ga[e] = in ? a.alpha_log[(cr.row0 + t) * a.H + h] : 0.f;
+                gb[e] = in ? a.beta[(cr.row0 + t) * a.H + h] : 0.f;
+            }
+            scan_gates<false>(gv, bt, nullptr, a.scale, ga, gb, lane);
+        } else if (warp == 9) {
+            const float4* src = reinterpret_cast<const float4*>(a.blk + ((size_t)n * a.H + h) * kBwdBytes + kBwdImg);
+            float4 v[(kBwdRecBytes / 16 + 31) / 32];
+#pragma unroll
+            for (int e = 0; e < (int)(kBwdRecBytes / 16 + 31) / 32; ++e)
+                if (lane + 32 * e < (int)kBwdRecBytes / 16) v[e] = src[lane + 32 * e];
+#pragma unroll
+            for (int e = 0; e < (int)(kBwdRecBytes / 16 + 31) / 32; ++e)
+                if (lane + 32 * e < (int)kBwdRecBytes / 16) reinterpret_cast<float4*>(rec)[lane + 32 * e] = v[e];
+        } else if (warp >= 10 && warp < 14) {
+            const float* from = warp == 10 ? a.po : warp == 11 ? a.px : warp == 12 ? a.pb : a.pw;
+            const float2* p = reinterpret_cast<const float2*>(from + ((size_t)n * a.H + h) * SL * 4 * kChunk) + lane;
+            float2 t = make_float2(0.f, 0.f);
+            for (int k = 0; k < 4 * SL; k += 8) {  // SL is 2 or 4
+                float2 v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = p[(k + e) * 32];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    t.x += v[e].x;
+                    t.y += v[e].y;
+                }
+            }
+            reinterpret_cast<float2*>(gs + 64 * (warp - 10))[lane] = t;
+        } else if (warp == 14) {
+            float end = a.gs[((size_t)n * a.H + h) * SL * 16 + lane];
+            if (SL == 4) end += a.gs[((size_t)n * a.H + h) * SL * 16 + 32 + lane];
+#pragma unroll
+            for (int o = 16; o; o >>= 1) end += __shfl_xor_sync(0xffffffffu, end, o);
+            if (lane == 0) gs[256] = end;
+        }
+    };
+    head_scalars(hk * rep);
 
     bool ok = wait_bar(&bars[0], 0, abort_flag);
     if (a.cu_s && cr.valid < kChunk) {
@@ -151,20 +202,6 @@ grads_kernel(const __grid_constant__ GradMaps tm, const Args a)
         for (int hh = 0; hh < rep; ++hh) {
             const int h = hk * rep + hh;
             const size_t hcn = (size_t)n * a.H + h;
-            if (warp == 4) {  // gates of the head
-                float ga[2], gb[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int t = 2 * lane + e;
-                    const bool in = t < cr.valid;
-                    ga[e] = in ? a.alpha_log[(cr.row0 + t) * a.H + h] : 0.f;
-                    gb[e] = in ? a.beta[(cr.row0 + t) * a.H + h] : 0.f;
-                }
-                scan_gates<false>(gv, bt, nullptr, a.scale, ga, gb, lane);
-            } else if (warp == 5) {
-                const float4* src = reinterpret_cast<const float4*>(a.blk + hcn * kBwdBytes + kBwdImg);
-                for (int e = lane; e < (int)kBwdRecBytes / 16; e += 32) reinterpret_cast<float4*>(rec)[e] = src[e];
-            }
             if (warp == 0) {
                 ok = wait_bar(&bars[1], hh & 1, abort_flag);
                 tc_fence_after_sync();
@@ -186,50 +223,52 @@ grads_kernel(const __grid_constant__ GradMaps tm, const Args a)
             ok = wait_bar(&bars[3], hh & 1, abort_flag) && ok;
             if (!(ok = __syncthreads_and(ok))) break;
             tc_fence_after_sync();
-            if (warp < 4) {
-                // ---- rows of -M2 (lanes 0..63) and M1, and their sums for dalpha_log
-                const int r = tid & 63, R = r >> 4;
-                const bool m1 = warp >= 2, live = r < cr.valid;
-                const float ph = gv.at(kP, r), pl = gv.at(kPlo, r), lead = m1 ? a.scale : 1.f;
-                float fd[16];
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const float4 p4 = gv.get4(kP, 4 * R + g), l4 = gv.get4(kPlo, 4 * R + g);
-                    const float4 b4 = gv.get4(kBeta, 4 * R + g);
-                    const float pv[4] = {p4.x, p4.y, p4.z, p4.w}, lv[4] = {l4.x, l4.y, l4.z, l4.w};
-                    const float bv[4] = {b4.x, b4.y, b4.z, b4.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) fd[4 * g + e] = lead * bv[e] * __expf((ph - pv[e]) + (pl - lv[e]));
-                }
-                const float ep = expf(ph);
-                float off = lead * fmaf(ep, pl, ep), sum = 0.f;
-                const int last = r & 15;
-                uint8_t* dst = sm + (m1 ? M1 : M2);
-#pragma unroll
-                for (int I = 3; I >= 0; --I) {
-                    if (I > ((warp & 1) ? 3 : 1)) continue;
+            // ---- rows of -M2 (lanes 0..63) and M1, and the sums of Z: a warp takes 32 rows and one
+            // of the column blocks on or left of their diagonal blocks (two, or four)
+            {
+                const int r = (quad & 1) * 32 + lane, R = r >> 4, I = warp >> 2;
+                const bool m1 = quad >= 2, live = r < cr.valid, diag = I >= 2 * (quad & 1);
+                if ((quad & 1) || I < 2) {
+                    const float lead = m1 ? a.scale : 1.f;
+                    const float ph = gv.at(kP, r), pl = gv.at(kPlo, r), ep = expf(ph);
+                    float off = lead * fmaf(ep, pl, ep);
+                    // whole blocks between this column block and the row's
+                    if (R > I + 1) off *= bt[I + 1];
+                    if (R > I + 2) off *= bt[I + 2];
+                    const int last = I == R ? (r & 15) : I < R ? 16 : -1;  // columns before this one count
                     float g[16], p[16], q[16];
                     tmem_ld16(tq + TM_G + 16 * I, g);
                     tmem_ld16(tq + TM_P + 16 * I, p);
-                    tmem_ld16(tq + TM_PL + 16 * I, q);
+                    if (!m1) tmem_ld16(tq + TM_PL + 16 * I, q);
                     tmem_wait_ld();
+                    float sum = 0.f;
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const float4 s4 = gv.get4(kSbeta, 4 * I + x);
-                        const float sv[4] = {s4.x, s4.y, s4.z, s4.w};
+                    for (int y = 0; y < 4; ++y) {
+                        const float4 s4 = gv.get4(kSbeta, 4 * I + y);
+                        float f[4] = {off * s4.x, off * s4.y, off * s4.z, off * s4.w};
+                        if (diag) {  // the warp's rows include this block's diagonal
+                            const float4 p4 = gv.get4(kP, 4 * I + y), l4 = gv.get4(kPlo, 4 * I + y);
+                            const float4 b4 = gv.get4(kBeta, 4 * I + y);
+                            const float pv[4] = {p4.x, p4.y, p4.z, p4.w}, lv[4] = {l4.x, l4.y, l4.z, l4.w};
+                            const float bv[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float d = lead * bv[e] * __expf((ph - pv[e]) + (pl - lv[e]));
+                                f[e] = I == R ? d : f[e];
+                            }
+                        }
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int j = 4 * x + e;
-                            const float f = I == R ? fd[j] : off * sv[e];
-                            const bool in = live && (I < R || (I == R && (m1 ? j <= last : j < last)));
-                            const float t = m1 ? p[j] : p[j] + q[j];
-                            p[j] = in ? (m1 ? f * t : -f * t) : 0.f;
+                            const int j = 4 * y + e;
+                            const bool in = live && (m1 && I == R ? j <= last : j < last);
+                            const float t = m1 ? p[j] : -(p[j] + q[j]);
+                            p[j] = in ? f[e] * t : 0.f;
                             // Z, without the diagonal (M1's own: a token's decay does not act on itself)
-                            g[j] = I < R || (I == R && j < last) ? (live ? p[j] * g[j] : 0.f) : 0.f;
+                            g[j] = live && j < last ? p[j] * g[j] : 0.f;
                             sum += g[j];
                         }
                     }
-                    if (I < R) off *= bt[I];
+                    uint8_t* dst = sm + (m1 ? M1 : M2);
                     st_bf16x8(dst + sw128_off(r, 2 * I), p);
                     st_bf16x8(dst + sw128_off(r, 2 * I + 1), p + 8);
                     // column sums over the warp's 32 rows: halve the columns a lane holds per step
@@ -243,28 +282,27 @@ grads_kernel(const __grid_constant__ GradMaps tm, const Args a)
                         }
                     }
                     g[0] += __shfl_xor_sync(0xffffffffu, g[0], 16);
-                    if (lane < 16) cs[128 + 64 * warp + 16 * I + lane] = g[0];
+                    if (lane < 16) cs[kCsCols + 64 * quad + 16 * I + lane] = g[0];
+                    rows[I * 128 + quad * 32 + lane] = sum;
+                } else {  // no columns right of the warp's rows
+                    if (lane < 16) cs[kCsCols + 64 * quad + 16 * I + lane] = 0.f;
+                    rows[I * 128 + quad * 32 + lane] = 0.f;
                 }
-                // columns right of the warp's rows
-                if (!(warp & 1)) cs[128 + 64 * warp + 32 + lane] = 0.f;
-                cs[(m1 ? 0 : 64) + r] = sum;
                 tc_fence_before_sync();
-            } else {
-                // ---- Diag(D) dv (negated), Diag(Dq) dO, Diag(gam) Vtilde in place
-                const int t = tid - 128;
-#pragma unroll 4
-                for (int e = t; e < 3 * 64 * 16; e += 128) {
-                    const int which = e >> 10, r = (e >> 4) & 63, c = e & 15;
-                    uint8_t* at = which == 0   ? sm + DV + (c >> 3) * 16384 + sw128_off(r, c & 7)
-                                  : which == 1 ? sm + DV + 8192 + (c >> 3) * 16384 + sw128_off(r, c & 7)
-                                               : sm + VT + (c >> 3) * 8192 + sw128_off(r, c & 7);
-                    const float f = which == 0 ? -rec[kRecD + r] : which == 1 ? rec[kRecDq + r] : rec[kRecGam + r];
-                    float x[8];
-                    unpack_bf16x8(*reinterpret_cast<const uint4*>(at), x);
+            }
+            // ---- Diag(D) dv (negated), Diag(Dq) dO, Diag(gam) Vtilde in place
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) x[k] *= f;
-                    st_bf16x8(at, x);
-                }
+            for (int e = tid; e < 3 * 64 * 16; e += kThreads) {
+                const int which = e >> 10, r = (e >> 4) & 63, c = e & 15;
+                uint8_t* at = which == 0   ? sm + DV + (c >> 3) * 16384 + sw128_off(r, c & 7)
+                              : which == 1 ? sm + DV + 8192 + (c >> 3) * 16384 + sw128_off(r, c & 7)
+                                           : sm + VT + (c >> 3) * 8192 + sw128_off(r, c & 7);
+                const float f = which == 0 ? -rec[kRecD + r] : which == 1 ? rec[kRecDq + r] : rec[kRecGam + r];
+                float x[8];
+                unpack_bf16x8(*reinterpret_cast<const uint4*>(at), x);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] *= f;
+                st_bf16x8(at, x);
             }
             fence_proxy_async_smem();
             __syncthreads();
@@ -301,27 +339,20 @@ grads_kernel(const __grid_constant__ GradMaps tm, const Args a)
                 mma_commit_elect(&bars[4]);
             } else if (warp == 1) {
                 // ---- the head's gate gradients
-                float c[2] = {0.f, 0.f}, b[2] = {0.f, 0.f}, w_[2] = {0.f, 0.f};
-                const float2* po = reinterpret_cast<const float2*>(a.po + hcn * SL * 4 * kChunk);
-                const float2* px = reinterpret_cast<const float2*>(a.px + hcn * SL * 4 * kChunk);
-                const float2* pb = reinterpret_cast<const float2*>(a.pb + hcn * SL * 4 * kChunk);
-                const float2* pw = reinterpret_cast<const float2*>(a.pw + hcn * SL * 4 * kChunk);
-                for (int k = 0; k < 4 * SL; ++k) {
-                    const float2 u = po[k * 32 + lane], v = px[k * 32 + lane], w = pb[k * 32 + lane];
-                    const float2 y = pw[k * 32 + lane];
-                    c[0] += u.x - v.x; c[1] += u.y - v.y;
-                    b[0] += w.x; b[1] += w.y;
-                    w_[0] += y.x; w_[1] += y.y;
-                }
-                float end = 0.f;
-                for (int k = lane; k < 16 * SL; k += 32) end += a.gs[hcn * SL * 16 + k];
-#pragma unroll
-                for (int o = 16; o; o >>= 1) end += __shfl_xor_sync(0xffffffffu, end, o);
+                float c[2], b[2], w_[2];
+                const float end = gs[256];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int r = 2 * lane + e;
-                    c[e] += (cs[r] + cs[64 + r]) -
-                            ((cs[128 + r] + cs[192 + r]) + (cs[256 + r] + cs[320 + r]));
+                    float rs = 0.f, col = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        rs += rows[k * 128 + r] + rows[k * 128 + 64 + r];
+                        col += cs[kCsCols + 64 * k + r];
+                    }
+                    c[e] = (gs[r] - gs[64 + r]) + (rs - col);
+                    b[e] = gs[128 + r];
+                    w_[e] = gs[192 + r];
                     if (r >= cr.valid) c[e] = w_[e] = 0.f;
                 }
                 float pre = w_[0] + w_[1];  // inclusive prefix sum over lanes
@@ -358,23 +389,21 @@ grads_kernel(const __grid_constant__ GradMaps tm, const Args a)
                 load_states(h + 1);
                 loads = hh + 2;
             }
+            if (hh + 1 < rep) head_scalars(h + 1);
         }
     }
     if (ok) {
-        // ---- dq, dk: bf16 through the rows' tile, 64 columns of 16 rows a warp
-        const int r0 = quad * 16 + (lane >> 2), pc = (lane & 3) * 4, half = warp >> 2;
+        // ---- dq, dk: bf16 through the rows' tile; a warp 64 columns of 16 rows of one of them
+        const int r0 = quad * 16 + (lane >> 2), pc = (lane & 3) * 4, half = (warp >> 2) & 1, w = warp >> 3;
+        float x[32];
+        tmem_ld_16x256<8>(tq + (w ? TM_K : TM_Q) + 64 * half, x);
+        tmem_wait_ld();
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            float x[32];
-            tmem_ld_16x256<8>(tq + (w ? TM_K : TM_Q) + 64 * half, x);
-            tmem_wait_ld();
+        for (int c = 0; c < 8; ++c)
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    *reinterpret_cast<uint32_t*>(sm + DV + w * 16384 + half * 8192 + sw128_off(r0 + 8 * e, c) + pc) =
-                        pack_bf16(x[4 * c + 2 * e], x[4 * c + 2 * e + 1]);
-        }
+            for (int e = 0; e < 2; ++e)
+                *reinterpret_cast<uint32_t*>(sm + DV + w * 16384 + half * 8192 + sw128_off(r0 + 8 * e, c) + pc) =
+                    pack_bf16(x[4 * c + 2 * e], x[4 * c + 2 * e + 1]);
         fence_proxy_async_smem();
         tc_fence_before_sync();
         __syncthreads();
@@ -386,7 +415,7 @@ grads_kernel(const __grid_constant__ GradMaps tm, const Args a)
                     tma_store_4d(&tm.dk, p * 64, hk, tt, tb, sm + DV + 16384 + p * 8192);
                 }
                 bulk_commit_group();
-                bulk_wait_group_all();
+                bulk_wait_group_read<0>();
             }
         } else {
             for (int e = tid; e < 2 * 64 * 16; e += kThreads) {
@@ -412,12 +441,6 @@ grads_kernel(const __grid_constant__ GradMaps tm, const Args a)
     }
 }
 
-// [chunks * H] matrices d x d, bf16; box = {64, 128, 1}
-bool make_state_map(CUtensorMap* map, const void* base, const Args& a)
-{
-    return make_chunk_map(map, base, chunks(a) * a.H, D, D, D);
-}
-
 }  // namespace
 
 cudaError_t launch_rebuild_tc(const Args& a, int ns, cudaStream_t s);
@@ -435,7 +458,7 @@ cudaError_t launch_bwd_tc(const Args& a, cudaStream_t s)
         !make_rows_map(&m.vt, a.vt, a, a.H, 64, sw) || !make_rows_map(&m.d_o, a.d_o, a, a.H, 64, sw) ||
         !make_rows_map(&m.dv, a.dv, a, a.H, 64, sw) || !make_rows_map(&m.dvl, a.dvl, a, a.H, 64, sw) ||
         !make_rows_map(&m.dq, a.dq, a, a.Hk, 64, sw) || !make_rows_map(&m.dk, a.dk, a, a.Hk, 64, sw) ||
-        !make_state_map(&m.s, a.sb, a) || !make_state_map(&m.g, a.gb, a))
+        !make_states_map(&m.s, a.sb, a, 64, sw) || !make_states_map(&m.g, a.gb, a, 64, sw))
         return cudaErrorInvalidValue;
     if ((e = cudaFuncSetAttribute(grads_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)BYTES)) !=
         cudaSuccess)

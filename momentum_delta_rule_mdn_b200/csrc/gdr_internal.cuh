@@ -62,7 +62,7 @@ struct Args {
     float* ssf = nullptr;            // [SL][16 warps][ns / 4][32]  entering state, in thread order
     __nv_bfloat16* sb = nullptr;     // [d, d]  entering state
     __nv_bfloat16* gb = nullptr;     // [d, d]  adjoint of the leaving state
-    float* xs = nullptr;             // [SL][64][ns]  Diag(D) K S
+    float* xs = nullptr;             // [SL][16 warps][ns / 32][32][4]  Diag(D) K S, in thread order
     float* po = nullptr;             // [SL][4][64]  scale D_r (S^T q_r) . do_r over 1/4 of the slice
     float* px = nullptr;             // [SL][4][64]  XS . dv
     float* pb = nullptr;             // [SL][4][64]  vtilde . dv / beta  (dbeta)

@@ -446,6 +446,20 @@ bool make_rows_map(CUtensorMap* map, const void* base, const Args& a, int heads,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_states_map(CUtensorMap* map, const void* base, const Args& a, int box_d, CUtensorMapSwizzle swizzle)
+{
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t d = (cuuint64_t)a.D;
+    cuuint64_t dims[3] = {d, d, (cuuint64_t)(chunks(a) * a.H)};
+    cuuint64_t strides[2] = {d * 2, d * d * 2};
+    cuuint32_t box[3] = {(cuuint32_t)box_d, (cuuint32_t)a.D, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t launch_operands_tc(const Args& a, cudaStream_t s, bool bwd)
 {
     if (bwd) return launch_typed<128, true>(a, s);

@@ -3,7 +3,7 @@
 //     S <- aC S + K^T [gV_hi | gV_lo],     gV = Diag(gam) Vtilde,
 // and, while it has each entering state in two bf16 terms, forms what needs it in
 // full precision (the fp32 gate gradients):
-//     A1 = [K; Q] [S_hi | S_lo]            (M 128, N 2 NS, K 128)
+//     A1 = K [S_hi | S_lo], Q [S_hi | S_lo]    (each M 64, N 2 NS, K 128)
 //     XS = Diag(D) K S                     fp32, for the reverse chain's <XS, dv>
 //     rows of scale Diag(D) (Q S) . dO     summed over the slice's columns
 // The products of the update do not depend on the state, so nothing but the fp32
@@ -12,8 +12,9 @@
 // epilogues) and, for the outputs, by L2: per chunk and head 64 KB of fp32 states
 // (for <G, S>), 32 KB of bf16 states (for the token gradients) and 32 KB of XS.
 //
-// Warps: 0 MMA issue, 1 loads, 16 chain warps (the state as in the forward chain;
-// of A1, lane quadrants 0, 1 hold K S and 2, 3 hold Q S), 4 warps that form gV.
+// Warps: 0 MMA issue, 1 loads, 16 chain warps (the state, K S and Q S as in the forward
+// chain), 4 warps that form gV, 1 that stores the bf16 states (TMA from a tile of their
+// own: 16-byte pieces from the chain warps, 32 rows an instruction, held them up).
 #include "gdr_tc.cuh"
 
 namespace mdn {
@@ -27,16 +28,17 @@ using inter::warp_wait;
 
 constexpr int D = 128;
 constexpr int kChainWarp0 = 2, CW = 16, kAuxWarp0 = kChainWarp0 + CW, AW = 4;
-constexpr int kThreads = (kAuxWarp0 + AW) * 32;
-constexpr int NV = 2;  // slots of Vtilde, dO and the record
+constexpr int kStoreWarp = kAuxWarp0 + AW, kThreads = (kStoreWarp + 1) * 32;
 
 template <int NS>
 struct Cfg {
     static constexpr int NH = NS / 4;
+    static constexpr int NV = NS == 32 ? 4 : 2;              // slots of Vtilde, dO and the record
     static constexpr uint32_t KQ0 = 0;                       // [K; Q], 2 slots
     static constexpr uint32_t ST0 = 2 * 32768;               // [S_hi | S_lo], 2 slots
     static constexpr uint32_t ST_BYTES = D * 2 * NS * 2;
-    static constexpr uint32_t GV0 = ST0 + 2 * ST_BYTES;      // [gV_hi | gV_lo], 2 slots
+    static constexpr uint32_t SI = ST0 + 2 * ST_BYTES;       // the entering state in bf16, to be stored
+    static constexpr uint32_t GV0 = SI + D * NS * 2;         // [gV_hi | gV_lo], 2 slots
     static constexpr uint32_t GV_BYTES = 64 * 2 * NS * 2;
     static constexpr uint32_t V_BYTES = 64 * NS * 2;
     static constexpr uint32_t V0 = GV0 + 2 * GV_BYTES;       // Vtilde slice, NV slots
@@ -46,7 +48,7 @@ struct Cfg {
     static constexpr uint32_t MISC = BARS + 256;
     static constexpr uint32_t BYTES = MISC + 16;
     static_assert(BYTES <= 232448, "shared memory");
-    static constexpr uint32_t TM_A1 = 0;        // 2 slots x 2 NS
+    static constexpr uint32_t TM_A1 = 0;        // K S, then Q S: 2 NS each
     static constexpr uint32_t TM_A2 = 4 * NS;   // 2 slots x 2 NS
     static constexpr uint32_t kTmemCols = 8 * NS;
     __device__ static __forceinline__ uint32_t off(int i, int c, int lo, uint32_t panel) {
@@ -58,24 +60,25 @@ struct Cfg {
 };
 
 constexpr int B_FKQ = 0;   // [2] K, Q landed
-constexpr int B_FVD = 2;   // [NV] Vtilde, dO, record landed
-constexpr int B_EVD = 4;   // [NV] ... read
-constexpr int B_M1 = 6;    // [2] A1 complete (and the A2 before it: the K, Q slot is free)
-constexpr int B_M2 = 8;    // [2] A2 complete
-constexpr int B_GV = 10;   // [2] gV written
-constexpr int B_SR = 12;   // [2] next state written
-constexpr int B_OD = 14;   // [2] A1 slot read
-constexpr int B_FIN = 16;
-constexpr int kBars = 17;
+constexpr int B_FVD = 2;   // [4] Vtilde, dO, record landed
+constexpr int B_EVD = 6;   // [4] ... read
+constexpr int B_M1 = 10;   // [2] A1 complete
+constexpr int B_M2 = 12;   // [2] A2 complete (and the A1 before it)
+constexpr int B_GV = 14;   // [2] gV written
+constexpr int B_SR = 16;   // [2] next state written
+constexpr int B_OD = 18;   //     A1 read
+constexpr int B_SF = 19;   //     the bf16 state's tile has been stored
+constexpr int B_FIN = 20;
+constexpr int kBars = 21;
 
 template <int NS>
 __global__ void __launch_bounds__(kThreads, 1)
 rebuild_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                const __grid_constant__ CUtensorMap tm_vt, const __grid_constant__ CUtensorMap tm_do,
-               const Args a)
+               const __grid_constant__ CUtensorMap tm_sb, const Args a)
 {
     using L = Cfg<NS>;
-    constexpr int NH = L::NH, NP = NH / 8, SL = D / NS;
+    constexpr int NH = L::NH, NP = NH / 8, SL = D / NS, NV = L::NV;
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sbase = smem_u32(sm);
     const int tid = threadIdx.x, lid = tid & 31;
@@ -95,7 +98,7 @@ rebuild_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             uint32_t count = 1;
             if (k >= B_EVD && k < B_EVD + NV) count = CW + AW;
             if (k >= B_GV && k < B_GV + 2) count = AW;
-            if (k >= B_SR && k < B_OD + 2) count = CW;
+            if (k >= B_SR && k <= B_OD) count = CW;
             mbar_init(&bars[k], count);
         }
         mbar_fence_init();
@@ -118,16 +121,14 @@ rebuild_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             const int cc = hc * NP + c;
             *reinterpret_cast<uint4*>(sm + L::ST0 + slot * L::ST_BYTES + L::off(irow, cc, 0, D * 128)) = hi;
             *reinterpret_cast<uint4*>(sm + L::ST0 + slot * L::ST_BYTES + L::off(irow, cc, 1, D * 128)) = lo;
+            *reinterpret_cast<uint4*>(sm + L::SI + L::v_off(irow, cc)) = hi;
         }
     };
-    auto store_state = [&](int n) {  // fp32 in the order these threads hold it, and bf16 rows
+    auto store_state = [&](int n) {  // fp32, in the order these threads hold it
         float* dst = a.ssf + ((head_chunk(n) * SL + slice) * CW + (warp - kChainWarp0)) * (NH * 32) + 4 * lid;
 #pragma unroll
         for (int j = 0; j < NH; j += 4)
             *reinterpret_cast<float4*>(dst + 32 * j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
-#pragma unroll
-        for (int c = 0; c < NP; ++c)
-            *reinterpret_cast<uint4*>(a.sb + (head_chunk(n) * D + irow) * D + j0 + NH * hc + 8 * c) = bf16x8(s + 8 * c);
     };
     const size_t srow0 = ((size_t)ch.state * D + irow) * D + j0 + NH * hc;
     if (chain) {
@@ -153,9 +154,9 @@ rebuild_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const uint64_t d_kt0 = smem_desc(sbase + L::KQ0, 16384, 1024, kSw128);  // MN-major
         const uint64_t d_st0 = smem_desc(sbase + L::ST0, D * 128, 1024, kSw128);
         const uint64_t d_gv0 = smem_desc(sbase + L::GV0, 8192, 1024, kSw128);
-        constexpr uint32_t id1 = idesc_bf16(128, 2 * NS, false, true);
+        constexpr uint32_t id1 = idesc_bf16(64, 2 * NS, false, true);
         constexpr uint32_t id2 = idesc_bf16(128, 2 * NS, true, true);
-        auto update = [&](int n) {  // A2 of chunk n; its slot was read before SR of n - 2
+        auto update = [&](int n) {  // A2 of chunk n; its TMEM slot was read before SR of n - 2
             const int s2 = n & 1;
             if (!warp_wait(&bars[B_FKQ + s2], (n >> 1) & 1, abort_flag)) return false;
             if (!warp_wait(&bars[B_GV + s2], (n >> 1) & 1, abort_flag)) return false;
@@ -172,15 +173,18 @@ rebuild_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         for (int n = 0; n < NT && go; ++n) {
             const int s2 = n & 1;
             if (n >= 1 && !warp_wait(&bars[B_SR + (s2 ^ 1)], ((n - 1) >> 1) & 1, abort_flag)) break;
-            if (n + 1 < NT && !update(n + 1)) break;
-            if (n >= 2 && !warp_wait(&bars[B_OD + s2], ((n - 2) >> 1) & 1, abort_flag)) break;
+            if (n >= 1 && !warp_wait(&bars[B_OD], (n - 1) & 1, abort_flag)) break;
             tc_fence_after_sync();
             const uint64_t dk = d_k0 + s2 * (32768 >> 4), dst = d_st0 + s2 * (L::ST_BYTES >> 4);
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-                mma_bf16_elect(tmem + L::TM_A1 + 2 * NS * s2, dk + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
-                               dst + ks * (2048 >> 4), id1, ks > 0);
+            for (int ks = 0; ks < 8; ++ks) {
+                const uint64_t d = dk + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4);
+                mma_bf16_elect(tmem + L::TM_A1, d, dst + ks * (2048 >> 4), id1, ks > 0);
+                mma_bf16_elect(tmem + L::TM_A1 + 2 * NS, d + (8192 >> 4), dst + ks * (2048 >> 4), id1, ks > 0);
+            }
             mma_commit_elect(&bars[B_M1 + s2]);
+            // the next update needs no state; the state it follows is one epilogue away
+            if (n + 1 < NT && !update(n + 1)) break;
         }
         mma_commit_elect(&bars[B_FIN]);
         (void)mbar_wait(&bars[B_FIN], 0);
@@ -191,7 +195,7 @@ rebuild_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             int done_kq = 0, done_vd = 0;
             for (int n = 0; n < NT; ++n) {
                 const int s2 = n & 1, sv = n % NV, t = tt0 + n * kChunk;
-                if (n >= 2 && !wait_bar(&bars[B_M1 + s2], ((n - 2) >> 1) & 1, abort_flag)) break;
+                if (n >= 2 && !wait_bar(&bars[B_M1 + s2], ((n - 2) >> 1) & 1, abort_flag)) break;  // A2 came before
                 uint64_t* fb = &bars[B_FKQ + s2];
                 mbar_arrive_expect_tx(fb, 32768);
 #pragma unroll
@@ -218,20 +222,20 @@ rebuild_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         __syncwarp();
     } else if (chain) {
         // ------------------------------------------------------------ the state, and A1's epilogue
-        const int r = irow & 63;
-        const bool qpart = quad >= 2;
+        const int r0 = quad * 16 + (lid >> 2), pc = (lid & 3) * 4;
         for (int n = 0; n < NT; ++n) {
             const int s2 = n & 1, sv = n % NV;
             if (!warp_wait(&bars[B_FVD + sv], (n / NV) & 1, abort_flag)) break;
             const float* cr = reinterpret_cast<const float*>(sm + L::CR0 + sv * kBwdRecBytes);
-            const float aC = cr[kRecBwdB], dr = qpart ? cr[kRecDq + r] : cr[kRecD + r];
-            float od[NH];
-            if (qpart) {
+            const float aC = cr[kRecBwdB];
+            const float dr[2] = {cr[kRecD + r0], cr[kRecD + r0 + 8]}, dq[2] = {cr[kRecDq + r0], cr[kRecDq + r0 + 8]};
+            uint32_t ow[NP][2];
 #pragma unroll
-                for (int c = 0; c < NP; ++c)
-                    unpack_bf16x8(*reinterpret_cast<const uint4*>(sm + L::O0 + sv * L::V_BYTES +
-                                                                  L::v_off(r, hc * NP + c)), od + 8 * c);
-            }
+            for (int c = 0; c < NP; ++c)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    ow[c][e] = *reinterpret_cast<const uint32_t*>(sm + L::O0 + sv * L::V_BYTES +
+                                                                  L::v_off(r0 + 8 * e, hc * NP + c) + pc);
             __syncwarp();
             if (lid == 0) mbar_arrive(&bars[B_EVD + sv]);
             if (!warp_wait(&bars[B_M2 + s2], (n >> 1) & 1, abort_flag)) break;
@@ -249,8 +253,12 @@ rebuild_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
                 for (int j = 0; j < NH; ++j) s[j] = fmaf(aC, s[j], u[j] + w[j]);
             }
-            // the other slot's reader, A1 of chunk n - 1, was waited for below
-            if (n + 1 < NT) put_state(s2 ^ 1);
+            // the other slot's reader, A1 of chunk n - 1, was waited for below; the tile of
+            // the bf16 state has been stored
+            if (n + 1 < NT) {
+                if (!warp_wait(&bars[B_SF], n & 1, abort_flag)) break;
+                put_state(s2 ^ 1);
+            }
             fence_proxy_async_smem();
             tc_fence_before_sync();
             __syncwarp();
@@ -258,32 +266,51 @@ rebuild_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             if (n + 1 < NT) store_state(n + 1);
             if (!warp_wait(&bars[B_M1 + s2], (n >> 1) & 1, abort_flag)) break;
             tc_fence_after_sync();
-            float u[NH], w[NH];
-            if constexpr (NH == 8) {
-                tmem_ld8(tq + L::TM_A1 + 2 * NS * s2 + NH * hc, u);
-                tmem_ld8(tq + L::TM_A1 + 2 * NS * s2 + NS + NH * hc, w);
-            } else {
-                tmem_ld16(tq + L::TM_A1 + 2 * NS * s2 + NH * hc, u);
-                tmem_ld16(tq + L::TM_A1 + 2 * NS * s2 + NS + NH * hc, w);
-            }
+            float x[NP * 4], y[NP * 4], u[NP * 4], w[NP * 4];
+            tmem_ld_16x256<NP>(tq + L::TM_A1 + NH * hc, x);
+            tmem_ld_16x256<NP>(tq + L::TM_A1 + NS + NH * hc, y);
+            tmem_ld_16x256<NP>(tq + L::TM_A1 + 2 * NS + NH * hc, u);
+            tmem_ld_16x256<NP>(tq + L::TM_A1 + 3 * NS + NH * hc, w);
             tmem_wait_ld();
             tc_fence_before_sync();
             __syncwarp();
-            if (lid == 0) mbar_arrive(&bars[B_OD + s2]);
-            if (qpart) {
-                float x = 0.f;
+            if (lid == 0) mbar_arrive(&bars[B_OD]);
+            float po[2] = {0.f, 0.f};
+            float* xs = a.xs + ((head_chunk(n) * SL + slice) * CW + (warp - kChainWarp0)) * (NP * 128) + 4 * lid;
 #pragma unroll
-                for (int j = 0; j < NH; ++j) x = fmaf(u[j] + w[j], od[j], x);
-                a.po[(head_chunk(n) * SL + slice) * 4 * kChunk + hc * kChunk + r] = dr * x;
-            } else {
-                float* xs = a.xs + ((head_chunk(n) * SL + slice) * kChunk + r) * NS + NH * hc;
+            for (int c = 0; c < NP; ++c) {
 #pragma unroll
-                for (int j = 0; j < NH; j += 4)
-                    *reinterpret_cast<float4*>(xs + j) =
-                        make_float4(dr * (u[j] + w[j]), dr * (u[j + 1] + w[j + 1]),
-                                    dr * (u[j + 2] + w[j + 2]), dr * (u[j + 3] + w[j + 3]));
+                for (int e = 0; e < 2; ++e) {
+                    const int i = 4 * c + 2 * e;
+                    float o0, o1;
+                    unpack2(ow[c][e], o0, o1);
+                    po[e] = fmaf(u[i] + w[i], o0, fmaf(u[i + 1] + w[i + 1], o1, po[e]));
+                }
+                *reinterpret_cast<float4*>(xs + 128 * c) =
+                    make_float4(dr[0] * (x[4 * c] + y[4 * c]), dr[0] * (x[4 * c + 1] + y[4 * c + 1]),
+                                dr[1] * (x[4 * c + 2] + y[4 * c + 2]), dr[1] * (x[4 * c + 3] + y[4 * c + 3]));
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                po[e] += __shfl_xor_sync(0xffffffffu, po[e], 1);
+                po[e] += __shfl_xor_sync(0xffffffffu, po[e], 2);
+                if ((lid & 3) == 0)
+                    a.po[((head_chunk(n) * SL + slice) * 4 + hc) * kChunk + r0 + 8 * e] = dq[e] * po[e];
             }
         }
+    } else if (warp == kStoreWarp) {
+        // ------------------------------------------------------------ the bf16 states
+        for (int n = 0; n < NT; ++n) {
+            if (n >= 1 && !warp_wait(&bars[B_SR + ((n - 1) & 1)], ((n - 1) >> 1) & 1, abort_flag)) break;
+            if (lid == 0) {
+                tma_store_3d(&tm_sb, j0, 0, (int)head_chunk(n), sm + L::SI);
+                bulk_commit_group();
+                bulk_wait_group_read<0>();
+                mbar_arrive(&bars[B_SF]);
+            }
+            __syncwarp();
+        }
+        if (lid == 0) bulk_wait_group_all();
     } else {
         // ------------------------------------------------------------ gV
         const int ot = tid - kAuxWarp0 * 32, r = ot >> 1, h0 = (ot & 1) * (NS / 16);  // half a row each
@@ -335,17 +362,18 @@ template <int NS>
 cudaError_t launch_typed(const Args& a, cudaStream_t s)
 {
     using L = Cfg<NS>;
-    CUtensorMap mq, mk, mv, mo;
+    CUtensorMap mq, mk, mv, mo, ms;
     const auto sw = NS == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
     if (!make_rows_map(&mq, a.q, a, a.Hk, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_rows_map(&mk, a.k, a, a.Hk, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_rows_map(&mv, a.vt, a, a.H, NS, sw) || !make_rows_map(&mo, a.d_o, a, a.H, NS, sw))
+        !make_rows_map(&mv, a.vt, a, a.H, NS, sw) || !make_rows_map(&mo, a.d_o, a, a.H, NS, sw) ||
+        !make_states_map(&ms, a.sb, a, NS, sw))
         return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(rebuild_kernel<NS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)L::BYTES);
     if (e != cudaSuccess) return e;
     ProfScope ps(kGdrBwdStates, s);
-    rebuild_kernel<NS><<<(unsigned)(chains(a) * (D / NS)), kThreads, L::BYTES, s>>>(mq, mk, mv, mo, a);
+    rebuild_kernel<NS><<<(unsigned)(chains(a) * (D / NS)), kThreads, L::BYTES, s>>>(mq, mk, mv, mo, ms, a);
     return cudaGetLastError();
 }
 

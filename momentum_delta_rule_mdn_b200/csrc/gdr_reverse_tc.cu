@@ -28,7 +28,7 @@ using inter::warp_wait;
 
 constexpr int D = 128;
 constexpr int kChainWarp0 = 2, CW = 16, kOutWarp0 = kChainWarp0 + CW, OW = 4;
-constexpr int kThreads = (kOutWarp0 + OW) * 32;
+constexpr int kStoreWarp = kOutWarp0 + OW, kThreads = (kStoreWarp + 1) * 32;
 constexpr int NV = 2;  // slots of Vtilde, dO, the record
 
 template <int NS>
@@ -38,10 +38,14 @@ struct Cfg {
     static constexpr uint32_t KQ0 = 0;                        // [K; Q], 2 slots
     static constexpr uint32_t FB0 = 2 * 32768;                // T'_hi, Att'_hi, T'_lo, Att'_lo
     static constexpr uint32_t ST = FB0 + NFB * kBwdImg;       // [G_hi | G_lo]
-    static constexpr uint32_t YB = ST + D * 2 * NS * 2;       // E' terms, then -D dv terms
+    // G in bf16, to be stored by TMA (64 columns: no room, the chain warps store it)
+    static constexpr bool kTile = NS == 32;
+    static constexpr uint32_t GI = ST + D * 2 * NS * 2;
+    static constexpr uint32_t YB = GI + (kTile ? D * NS * 2 : 0);  // E' terms, then -D dv terms
     static constexpr uint32_t V_BYTES = 64 * NS * 2;
     static constexpr uint32_t EO = YB + 2 * V_BYTES;          // Dq dO terms
-    static constexpr uint32_t VB = EO + 2 * V_BYTES;          // bf16 dv and its rest
+    static constexpr int NEO = NS == 32 ? 2 : 1;              // its slots
+    static constexpr uint32_t VB = EO + NEO * 2 * V_BYTES;    // bf16 dv and its rest
     static constexpr uint32_t VL = VB + V_BYTES;
     static constexpr uint32_t V0 = VL + V_BYTES;              // Vtilde, NV slots
     static constexpr uint32_t O0 = V0 + NV * V_BYTES;         // dO, NV slots (an operand of R)
@@ -74,16 +78,19 @@ constexpr int B_YR = 12;   //     E' written
 constexpr int B_GR = 13;   //     -D dv written
 constexpr int B_VR = 14;   //     dv tiles written
 constexpr int B_SR = 15;   //     next adjoint written
-constexpr int B_EO = 16;   //     Dq dO written, rows behind the sequence cleared
-constexpr int B_VF = 17;   //     dv tiles stored
-constexpr int B_FIN = 18;
-constexpr int kBars = 19;
+constexpr int B_EO = 16;   // [2] Dq dO written, rows behind the sequence cleared (two: the first two
+                           //     chunks' are formed with nothing waited for in between)
+constexpr int B_VF = 18;   //     dv tiles stored
+constexpr int B_GF = 19;   //     the bf16 adjoint's tile has been stored
+constexpr int B_FIN = 20;
+constexpr int kBars = 21;
 
 template <int NS>
 __global__ void __launch_bounds__(kThreads, 1)
 reverse_kernel_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_vt, const __grid_constant__ CUtensorMap tm_do,
                   const __grid_constant__ CUtensorMap tm_dv, const __grid_constant__ CUtensorMap tm_dvl,
+                  const __grid_constant__ CUtensorMap tm_gb,
                   const Args a)
 {
     using L = Cfg<NS>;
@@ -107,7 +114,7 @@ reverse_kernel_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             uint32_t count = 1;
             if (k >= B_EVD && k < B_EVD + NV) count = CW + OW;
             if (k >= B_YR && k <= B_SR) count = CW;
-            if (k == B_EO || k == B_VF) count = OW;
+            if (k >= B_EO && k <= B_VF) count = OW;
             mbar_init(&bars[k], count);
         }
         mbar_fence_init();
@@ -129,6 +136,7 @@ reverse_kernel_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             const int cc = hc * NP + c;
             *reinterpret_cast<uint4*>(sm + L::ST + L::off(irow, cc, 0, D * 128)) = hi;
             *reinterpret_cast<uint4*>(sm + L::ST + L::off(irow, cc, 1, D * 128)) = lo;
+            if (L::kTile) *reinterpret_cast<uint4*>(sm + L::GI + L::v_off(irow, cc)) = hi;
         }
     };
     const size_t srow0 = ((size_t)ch.state * D + irow) * D + j0 + NH * hc;
@@ -168,7 +176,7 @@ reverse_kernel_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         auto rpart = [&](int m) {  // R of chunk m; its slot was read before SR of m - 2
             const int sf = m % L::NFB, sv = m % NV;
             if (!warp_wait(&bars[B_FFB + sf], (m / L::NFB) & 1, abort_flag)) return false;
-            if (!warp_wait(&bars[B_EO], m & 1, abort_flag)) return false;
+            if (!warp_wait(&bars[B_EO + (m & 1)], (m >> 1) & 1, abort_flag)) return false;
             tc_fence_after_sync();
             const uint64_t df = d_fb0 + sf * (kBwdImg >> 4), dO_ = d_o0 + sv * (L::V_BYTES >> 4);
 #pragma unroll
@@ -193,10 +201,11 @@ reverse_kernel_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                                d_st + ks * (2048 >> 4), id1, ks > 0);
             mma_commit_elect(&bars[B_M1]);
             // under the E' epilogue: Q^T Diag(Dq) dO
+            const uint64_t deo = d_eo + (m % L::NEO) * ((2 * L::V_BYTES) >> 4);
             const uint64_t dqt = d_qt0 + s2 * (32768 >> 4), dkt = d_kt0 + s2 * (32768 >> 4);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-                mma_bf16_elect(tmem + L::TM_A2, dqt + ks * (2048 >> 4), d_eo + ks * (2048 >> 4), id2, ks > 0);
+                mma_bf16_elect(tmem + L::TM_A2, dqt + ks * (2048 >> 4), deo + ks * (2048 >> 4), id2, ks > 0);
             if (!warp_wait(&bars[B_YR], m & 1, abort_flag)) break;
             tc_fence_after_sync();
 #pragma unroll
@@ -206,14 +215,17 @@ reverse_kernel_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             for (int ks = 0; ks < 4; ++ks)
                 mma_bf16_elect(tmem + L::TM_AT, df + (kBlkTlo >> 4) + ks * (2048 >> 4), d_y + ks * (2048 >> 4), idt, 1);
             mma_commit_elect(&bars[B_MT]);
+            // under the dv epilogue: R of the next chunk (with one slot of images, which it still
+            // waits for here, under the state's)
             if (m + 1 < NT && !warp_wait(&bars[B_FKQ + ((m + 1) & 1)], ((m + 1) >> 1) & 1, abort_flag)) break;
+            if (L::NFB == 2 && m + 1 < NT && !rpart(m + 1)) break;
             if (!warp_wait(&bars[B_GR], m & 1, abort_flag)) break;
             tc_fence_after_sync();
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
                 mma_bf16_elect(tmem + L::TM_A2, dkt + ks * (2048 >> 4), d_y + ks * (2048 >> 4), id2, 1);
             mma_commit_elect(&bars[B_M2 + s2]);
-            if (m + 1 < NT && !rpart(m + 1)) break;
+            if (L::NFB == 1 && m + 1 < NT && !rpart(m + 1)) break;
         }
         mma_commit_elect(&bars[B_FIN]);
         (void)mbar_wait(&bars[B_FIN], 0);
@@ -260,18 +272,22 @@ reverse_kernel_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         __syncwarp();
     } else if (chain) {
         // ------------------------------------------------------------ chain epilogues
-        const int r0 = quad * 16 + (lid >> 2), c2 = (lid & 3) * 2, pc = c2 * 2;
+        const int r0 = quad * 16 + (lid >> 2), pc = (lid & 3) * 4;
         for (int m = 0; m < NT; ++m) {
             const int n = NT - 1 - m, s2 = m & 1, sv = m % NV, valid = ch.len - n * kChunk;
             const size_t hcn = head_chunk(n);
             // XS of this thread's rows and columns
-            float2 xs[NP][2];
+            float4 xs[NP];
 #pragma unroll
             for (int c = 0; c < NP; ++c)
+                xs[c] = *reinterpret_cast<const float4*>(
+                    a.xs + ((hcn * SL + slice) * CW + (warp - kChainWarp0)) * (NP * 128) + 128 * c + 4 * lid);
+            float4 se[NH / 4];  // the state entering the chunk
+            {
+                const float* src = a.ssf + ((hcn * SL + slice) * CW + (warp - kChainWarp0)) * (NH * 32) + 4 * lid;
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    xs[c][e] = *reinterpret_cast<const float2*>(
-                        a.xs + ((hcn * SL + slice) * kChunk + r0 + 8 * e) * NS + NH * hc + 8 * c + c2);
+                for (int j = 0; j < NH / 4; ++j) se[j] = *reinterpret_cast<const float4*>(src + 128 * j);
+            }
             if (!warp_wait(&bars[B_FVD + sv], (m / NV) & 1, abort_flag)) break;
             const float* cr = reinterpret_cast<const float*>(sm + L::CR0 + sv * kBwdRecBytes);
             const float aC = cr[kRecBwdB];
@@ -331,19 +347,18 @@ reverse_kernel_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     if ((lid & 3) == 0)
                         a.pw[((hcn * SL + slice) * 4 + hc) * kChunk + r0 + 8 * e] = gu[e] * be[e] * pw[e];
                 }
-                const float* src = a.ssf + ((hcn * SL + slice) * CW + (warp - kChainWarp0)) * (NH * 32) + 4 * lid;
                 float t = 0.f;
 #pragma unroll
-                for (int j = 0; j < NH; j += 4) {
-                    const float4 sv4 = *reinterpret_cast<const float4*>(src + 32 * j);
-                    t = fmaf(g[j], sv4.x, fmaf(g[j + 1], sv4.y, fmaf(g[j + 2], sv4.z, fmaf(g[j + 3], sv4.w, t))));
-                }
+                for (int j = 0; j < NH; j += 4)
+                    t = fmaf(g[j], se[j / 4].x, fmaf(g[j + 1], se[j / 4].y,
+                        fmaf(g[j + 2], se[j / 4].z, fmaf(g[j + 3], se[j / 4].w, t))));
 #pragma unroll
                 for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
                 if (lid == 0) a.gs[(hcn * SL + slice) * CW + (warp - kChainWarp0)] = aC * t;
+                if (!L::kTile)
 #pragma unroll
-                for (int c = 0; c < NP; ++c)
-                    *reinterpret_cast<uint4*>(a.gb + (hcn * D + irow) * D + j0 + NH * hc + 8 * c) = bf16x8(g + 8 * c);
+                    for (int c = 0; c < NP; ++c)
+                        *reinterpret_cast<uint4*>(a.gb + (hcn * D + irow) * D + j0 + NH * hc + 8 * c) = bf16x8(g + 8 * c);
             }
             // the last chunk's dv has left
             if (m >= 1 && !warp_wait(&bars[B_VF], (m - 1) & 1, abort_flag)) break;
@@ -378,7 +393,7 @@ reverse_kernel_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     unpack2(vw[c][e], v0, v1);
                     pb[e] = fmaf(v0, x[i], fmaf(v1, x[i + 1], pb[e]));
                     const float d0 = be[e] * x[i], d1 = be[e] * x[i + 1];
-                    px[e] = fmaf(xs[c][e].x, d0, fmaf(xs[c][e].y, d1, px[e]));
+                    px[e] = e ? fmaf(xs[c].z, d0, fmaf(xs[c].w, d1, px[e])) : fmaf(xs[c].x, d0, fmaf(xs[c].y, d1, px[e]));
                     uint32_t hi, lo;
                     split2(d0, d1, hi, lo);
                     const uint32_t at = L::v_off(r0 + 8 * e, hc * NP + c) + pc;
@@ -415,11 +430,27 @@ reverse_kernel_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 #pragma unroll
                 for (int j = 0; j < NH; ++j) g[j] = fmaf(aC, g[j], u[j] + w[j]);
             }
+            if (L::kTile && !warp_wait(&bars[B_GF], m & 1, abort_flag)) break;
             put_state();
             fence_proxy_async_smem();
             tc_fence_before_sync();
             __syncwarp();
             if (lid == 0) mbar_arrive(&bars[B_SR]);
+        }
+    } else if (warp == kStoreWarp) {
+        // ------------------------------------------------------------ G in bf16
+        if (L::kTile) {
+            for (int m = 0; m < NT; ++m) {
+                if (m >= 1 && !warp_wait(&bars[B_SR], (m - 1) & 1, abort_flag)) break;
+                if (lid == 0) {
+                    tma_store_3d(&tm_gb, j0, 0, (int)head_chunk(NT - 1 - m), sm + L::GI);
+                    bulk_commit_group();
+                    bulk_wait_group_read<0>();
+                    mbar_arrive(&bars[B_GF]);
+                }
+                __syncwarp();
+            }
+            if (lid == 0) bulk_wait_group_all();
         }
     } else {
         // ------------------------------------------------------------ Dq dO, and the stores of dv
@@ -437,8 +468,9 @@ reverse_kernel_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             const int n = NT - 1 - m, s2 = m & 1, sv = m % NV, valid = ch.len - n * kChunk;
             if (!warp_wait(&bars[B_FVD + sv], (m / NV) & 1, abort_flag)) return false;
             const float q = reinterpret_cast<const float*>(sm + L::CR0 + sv * kBwdRecBytes)[kRecDq + r];
-            // its tile was read by the Q^T product of chunk m - 1 (A2 complete)
-            if (m >= 1 && !warp_wait(&bars[B_M2 + (s2 ^ 1)], ((m - 1) >> 1) & 1, abort_flag)) return false;
+            // its tile was read by the Q^T product of chunk m - NEO (A2 complete)
+            if (m >= L::NEO && !warp_wait(&bars[B_M2 + ((m - L::NEO) & 1)], ((m - L::NEO) >> 1) & 1, abort_flag)) return false;
+            uint8_t* eo = sm + L::EO + (m % L::NEO) * 2 * L::V_BYTES;
 #pragma unroll
             for (int c = 0; c < NS / 16; ++c) {
                 uint8_t* src = sm + L::O0 + sv * L::V_BYTES + L::v_off(r, h0 + c);
@@ -449,8 +481,8 @@ reverse_kernel_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 for (int e = 0; e < 8; ++e) x[e] = r < valid ? q * x[e] : 0.f;
                 uint4 hi, lo;
                 split8(x, hi, lo);
-                *reinterpret_cast<uint4*>(sm + L::EO + L::off(r, h0 + c, 0, 8192)) = hi;
-                *reinterpret_cast<uint4*>(sm + L::EO + L::off(r, h0 + c, 1, 8192)) = lo;
+                *reinterpret_cast<uint4*>(eo + L::off(r, h0 + c, 0, 8192)) = hi;
+                *reinterpret_cast<uint4*>(eo + L::off(r, h0 + c, 1, 8192)) = lo;
             }
             if (valid < kChunk && a.cu_s) {
                 if (!warp_wait(&bars[B_FKQ + s2], (m >> 1) & 1, abort_flag)) return false;
@@ -464,7 +496,7 @@ reverse_kernel_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             fence_proxy_async_smem();
             __syncwarp();
             if (lid == 0) {
-                mbar_arrive(&bars[B_EO]);
+                mbar_arrive(&bars[B_EO + s2]);
                 mbar_arrive(&bars[B_EVD + sv]);
             }
             return true;
@@ -472,6 +504,7 @@ reverse_kernel_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         bool go = NT > 0 && form(0);
         for (int m = 0; m < NT && go; ++m) {
             const int n = NT - 1 - m;
+            if (L::NEO == 2 && m + 1 < NT && !form(m + 1)) break;
             const int valid = min(kChunk, ch.len - n * kChunk);
             const bool whole = !a.cu_s || valid == kChunk;
             if (!warp_wait(&bars[B_VR], m & 1, abort_flag)) break;
@@ -490,7 +523,7 @@ reverse_kernel_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 mbar_arrive(&bars[B_VF]);
             }
             __syncwarp();
-            if (m + 1 < NT && !form(m + 1)) break;
+            if (L::NEO == 1 && m + 1 < NT && !form(m + 1)) break;
         }
         if (lid == 0) bulk_wait_group_all();
     }
@@ -514,18 +547,19 @@ template <int NS>
 cudaError_t launch_typed(const Args& a, cudaStream_t s)
 {
     using L = Cfg<NS>;
-    CUtensorMap mq, mk, mv, mo, mdv, mdl;
+    CUtensorMap mq, mk, mv, mo, mdv, mdl, mg;
     const auto sw = NS == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
     if (!make_rows_map(&mq, a.q, a, a.Hk, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_rows_map(&mk, a.k, a, a.Hk, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_rows_map(&mv, a.vt, a, a.H, NS, sw) || !make_rows_map(&mo, a.d_o, a, a.H, NS, sw) ||
-        !make_rows_map(&mdv, a.dv, a, a.H, NS, sw, 16) || !make_rows_map(&mdl, a.dvl, a, a.H, NS, sw, 16))
+        !make_rows_map(&mdv, a.dv, a, a.H, NS, sw, 16) || !make_rows_map(&mdl, a.dvl, a, a.H, NS, sw, 16) ||
+        !make_states_map(&mg, a.gb, a, NS, sw))
         return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(reverse_kernel_tc<NS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)L::BYTES);
     if (e != cudaSuccess) return e;
     ProfScope ps(kGdrBwdChain, s);
-    reverse_kernel_tc<NS><<<(unsigned)(chains(a) * (D / NS)), kThreads, L::BYTES, s>>>(mq, mk, mv, mo, mdv, mdl, a);
+    reverse_kernel_tc<NS><<<(unsigned)(chains(a) * (D / NS)), kThreads, L::BYTES, s>>>(mq, mk, mv, mo, mdv, mdl, mg, a);
     return cudaGetLastError();
 }
 

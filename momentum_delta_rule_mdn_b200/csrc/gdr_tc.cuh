@@ -212,6 +212,9 @@ __device__ __forceinline__ void scan_gates(const GateVec& gv, float* btot, float
 bool make_rows_map(CUtensorMap* map, const void* base, const Args& a, int heads, int box_d,
                    CUtensorMapSwizzle swizzle, int box_rows = kChunk);
 
+// The same over [chunks * H] d x d matrices; box = {box_d, d, 1}.
+bool make_states_map(CUtensorMap* map, const void* base, const Args& a, int box_d, CUtensorMapSwizzle swizzle);
+
 // The operand blocks of every chunk and head (a.blk).
 cudaError_t launch_operands_tc(const Args& a, cudaStream_t s, bool bwd);
 

@@ -57,6 +57,31 @@ def test_forward_and_gradients(shape, dtype, flags):
     check(g, ref)
 
 
+@pytest.mark.parametrize("B,T,H,Hk", [(4, 2048, 8, 8), (1, 3000, 2, 1), (5, 777, 16, 4), (1, 4100, 37, 37)])
+def test_many_chunks_both_paths(B, T, H, Hk):
+    """Sequences of many chunks with few and many chains: the tensor-core kernels against the
+    fp32 CUDA-core ones (2e-5 covers both sides' fp32 error, 4.5e-3 the bf16 roundings of the
+    one and 2^-8 / sqrt(3) of the other's stores: 6.8e-3), and no wait that ran out."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")
+    q, v, do = r(B, T, Hk, 128).to(BF16), r(B, T, H, 128).to(BF16), r(B, T, H, 128).to(BF16)
+    k = torch.nn.functional.normalize(r(B, T, Hk, 128), dim=-1).to(BF16)
+    al, be = -torch.nn.functional.softplus(r(B, T, H) - 3), torch.sigmoid(r(B, T, H))
+    S0, dST = 0.1 * r(B, H, 128, 128), 0.1 * r(B, H, 128, 128)
+    chk = E.MDN_CHECK_FINITE
+    a = mdn.gdr_chunk_fwd(q, k, v, al, be, None, S0, flags=chk)
+    b = mdn.gdr_chunk_fwd(q, k, v, al, be, None, S0, flags=chk | E.MDN_FORCE_SIMT)
+    ga = mdn.gdr_chunk_bwd(q, k, al, be, None, b[1], do, S0, dST, flags=chk)
+    gb = mdn.gdr_chunk_bwd(q, k, al, be, None, b[1], do, S0, dST, flags=chk | E.MDN_FORCE_SIMT)
+    both = dict(zip(("o", "vt", "S"), zip(a, b))) | {n: (ga[n], gb[n]) for n in ga}
+    bad = {}
+    for n, (x, y) in both.items():
+        e = float((x.double() - y.double()).norm() / y.double().norm())
+        if not e <= (6.8e-3 if x.dtype == BF16 else 2e-5):
+            bad[n] = e
+    assert not bad, bad
+
+
 @pytest.mark.parametrize("decay", [-12.0, 3.0])
 def test_extreme_decay(decay):
     """alpha close to 1 (nothing forgotten over the whole sequence), and alpha ~ e^-3

@@ -48,13 +48,15 @@ using namespace tc;
 using inter::wait_bar;
 using inter::warp_wait;
 
-constexpr int kChainWarp0 = 2, CW = 16, kOutWarp0 = kChainWarp0 + CW, OW = 4;
-constexpr int kThreads = (kOutWarp0 + OW) * 32;
+constexpr int kChainWarp0 = 2, OW = 4;
 constexpr int NVC = 4;  // slots of V and the record
 
 template <int D, int NS>
 struct Cfg {
-    static constexpr int NH = NS / 4;  // columns of a chain thread's state
+    static constexpr int NH = NS == 16 ? 8 : NS / 4;  // columns of a chain thread's state
+    static constexpr int CW = 4 * (NS / NH);          // chain warps
+    static constexpr int kOutWarp0 = kChainWarp0 + CW;
+    static constexpr int kThreads = (kOutWarp0 + OW) * 32;
     static constexpr int KP = D / 64;  // 64-column panels of K, Q
     static constexpr uint32_t KQ_BYTES = KP * 16384;
     static constexpr uint32_t KQ0 = 0;                        // [K; Q], 2 slots
@@ -77,12 +79,18 @@ struct Cfg {
     static constexpr uint32_t TM_QS = 4 * NS;        // 2 slots x NS
     static constexpr uint32_t TM_AO = 6 * NS;        // 2 slots x NS
     static constexpr uint32_t kTmemCols = 8 * NS;
+    // Right operands: rows of 2 NS x 2 bytes, hi and lo side by side (for NS 64 two panels),
+    // swizzled by the row length; Vtilde, V and o have rows of half that.
+    static constexpr uint32_t kSwY = NS == 16 ? kSw64 : kSw128, kSboY = NS == 16 ? 512 : 1024;
+    static constexpr uint32_t kSwV = NS == 16 ? kSw32 : NS == 32 ? kSw64 : kSw128, kSboV = NS * 16;
+    static constexpr uint32_t kRowStepY = NS == 16 ? 1024 : 2048;  // bytes of 16 rows (one panel)
     // 16-byte piece c (8 columns) of row i of the hi (lo = 0) or lo part of a right operand
     __device__ static __forceinline__ uint32_t off(int i, int c, int lo, uint32_t panel) {
-        return NS == 32 ? sw128_off(i, 4 * lo + c) : lo * panel + sw128_off(i, c);
+        return NS == 16 ? sw64_off(i, 2 * lo + c) : NS == 32 ? sw128_off(i, 4 * lo + c)
+                                                             : lo * panel + sw128_off(i, c);
     }
     __device__ static __forceinline__ uint32_t v_off(int r, int c) {
-        return NS == 32 ? sw64_off(r, c) : sw128_off(r, c);
+        return NS == 16 ? sw32_off(r, c) : NS == 32 ? sw64_off(r, c) : sw128_off(r, c);
     }
 };
 
@@ -116,13 +124,14 @@ __device__ __forceinline__ void ld_cols(uint32_t t, float* v) {
 }
 
 template <int D, int NS>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, NS>::kThreads, 1)
 chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
              const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
              const __grid_constant__ CUtensorMap tm_vt, const ChainArgs p)
 {
     using L = Cfg<D, NS>;
     constexpr int NH = L::NH, NP = NH / 8;  // NP: 8-column pieces of a chain thread
+    constexpr int CW = L::CW, kOutWarp0 = L::kOutWarp0;
     const Args& a = p.a;
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sbase = smem_u32(sm);
@@ -193,11 +202,11 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         // ------------------------------------------------------------ MMA issue (converged)
         const uint64_t d_k0 = smem_desc(sbase + L::KQ0, 16, 1024, kSw128);
         const uint64_t d_kt0 = smem_desc(sbase + L::KQ0, 16384, 1024, kSw128);  // MN-major
-        const uint64_t d_st = smem_desc(sbase + L::ST, D * 128, 1024, kSw128);
+        const uint64_t d_st = smem_desc(sbase + L::ST, D * 128, L::kSboY, L::kSwY);
         const uint64_t d_fb0 = smem_desc(sbase + L::FB0, 16, 1024, kSw128);
-        const uint64_t d_y = smem_desc(sbase + L::YB, 8192, 1024, kSw128);
-        const uint64_t d_v = NS == 32 ? smem_desc(sbase + L::VB, 4096, 512, kSw64)
-                                      : smem_desc(sbase + L::VB, 8192, 1024, kSw128);
+        const uint64_t d_y = smem_desc(sbase + L::YB, 8192, L::kSboY, L::kSwY);
+        const uint64_t d_v = smem_desc(sbase + L::VB, 64 * NS * 2, L::kSboV, L::kSwV);
+        constexpr uint32_t ystep = L::kRowStepY >> 4;
         constexpr uint32_t vstep = (16 * NS * 2) >> 4;
         constexpr uint32_t id1 = idesc_bf16(64, 2 * NS, false, true);
         constexpr uint32_t id2 = idesc_bf16(D, 2 * NS, true, true);
@@ -214,26 +223,26 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
                 mma_bf16_elect(tmem + L::TM_KS, dk + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
-                               d_st + ks * (2048 >> 4), id1, ks > 0);
+                               d_st + ks * ystep, id1, ks > 0);
             mma_commit_elect(&bars[B_M1]);
 #pragma unroll
             for (int ks = 0; ks < KS / 2; ++ks)
                 mma_bf16_elect(qs, dq + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
-                               d_st + ks * (2048 >> 4), ido, ks > 0);
+                               d_st + ks * ystep, ido, ks > 0);
             if (!warp_wait(&bars[B_FFB + s2], (n >> 1) & 1, abort_flag)) break;
             if (!warp_wait(&bars[B_YR], n & 1, abort_flag)) break;
             tc_fence_after_sync();
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-                mma_bf16_elect(tmem + L::TM_AT, dfb + ks * 2, d_y + ks * (2048 >> 4), id1, ks > 0);
+                mma_bf16_elect(tmem + L::TM_AT, dfb + ks * 2, d_y + ks * ystep, id1, ks > 0);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-                mma_bf16_elect(tmem + L::TM_AT, dfb + (kBlkTlo >> 4) + ks * 2, d_y + ks * (2048 >> 4), id1, 1);
+                mma_bf16_elect(tmem + L::TM_AT, dfb + (kBlkTlo >> 4) + ks * 2, d_y + ks * ystep, id1, 1);
             mma_commit_elect(&bars[B_MT]);
 #pragma unroll
             for (int ks = KS / 2; ks < KS; ++ks)
                 mma_bf16_elect(qs, dq + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
-                               d_st + ks * (2048 >> 4), ido, 1);
+                               d_st + ks * ystep, ido, 1);
             // what the next chunk's products need, while Vtilde is formed
             if (n + 1 < NT && !warp_wait(&bars[B_FKQ + ((n + 1) & 1)], ((n + 1) >> 1) & 1, abort_flag)) break;
             if (n >= 1 && !warp_wait(&bars[B_OD + ((n + 1) & 1)], ((n - 1) >> 1) & 1, abort_flag)) break;
@@ -242,7 +251,7 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             const uint64_t dkt = d_kt0 + s2 * (L::KQ_BYTES >> 4);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-                mma_bf16_elect(tmem + L::TM_A2, dkt + ks * (2048 >> 4), d_y + ks * (2048 >> 4), id2, ks > 0);
+                mma_bf16_elect(tmem + L::TM_A2, dkt + ks * (2048 >> 4), d_y + ks * ystep, id2, ks > 0);
             mma_commit_elect(&bars[B_M2 + s2]);
             if (!warp_wait(&bars[B_VR], n & 1, abort_flag)) break;
             tc_fence_after_sync();
@@ -485,7 +494,9 @@ cudaError_t launch_chain(const Args& a, cudaStream_t s)
 {
     using L = Cfg<D, NS>;
     CUtensorMap mq, mk, mv, mo, mvt;
-    const auto sw = NS == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+    const auto sw = NS == 16   ? CU_TENSOR_MAP_SWIZZLE_32B
+                    : NS == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                               : CU_TENSOR_MAP_SWIZZLE_128B;
     if (!make_rows_map(&mq, a.q, a, a.Hk, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_rows_map(&mk, a.k, a, a.Hk, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_rows_map(&mv, a.v, a, a.H, NS, sw) ||
@@ -497,13 +508,17 @@ cudaError_t launch_chain(const Args& a, cudaStream_t s)
     if (e != cudaSuccess) return e;
     ChainArgs p{a, a.blk};
     ProfScope ps(kGdrChain, s);
-    chain_kernel<D, NS><<<(unsigned)(chains(a) * (D / NS)), kThreads, L::BYTES, s>>>(mq, mk, mv, mo, mvt, p);
+    chain_kernel<D, NS><<<(unsigned)(chains(a) * (D / NS)), L::kThreads, L::BYTES, s>>>(mq, mk, mv, mo, mvt, p);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-// Chain width.  (Figures: see the table in the header comment of launch_fwd_tc.)
+// Chain width.  A chunk's step takes about 2.1k, 2.8k and 4.6k cycles with 16, 32 and
+// 64 columns per CTA: the narrowest slice whose CTAs all fit on the SMs at once has the
+// shortest chain; beyond that the widest, which takes the least SM time per chunk of a
+// head (FIGURES).  Packed sequences start longest first (the longest chain is the
+// critical path), so they keep 32 columns up to four waves.
 cudaError_t launch_fwd_tc(const Args& a, cudaStream_t s)
 {
     cudaError_t e = launch_operands_tc(a, s, false);
@@ -512,8 +527,10 @@ cudaError_t launch_fwd_tc(const Args& a, cudaStream_t s)
     if ((e = cudaGetDevice(&dev)) != cudaSuccess ||
         (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
         return e;
-    if (a.D == 64) return launch_chain<64, 32>(a, s);
-    return chains(a) * 4 <= sms ? launch_chain<128, 32>(a, s) : launch_chain<128, 64>(a, s);
+    const long long n = chains(a);
+    if (a.D == 64) return n * 4 <= sms ? launch_chain<64, 16>(a, s) : launch_chain<64, 32>(a, s);
+    if (n * 8 <= sms) return launch_chain<128, 16>(a, s);
+    return n * 4 <= (a.cu_s ? 4 * sms : sms) ? launch_chain<128, 32>(a, s) : launch_chain<128, 64>(a, s);
 }
 
 }  // namespace gdr

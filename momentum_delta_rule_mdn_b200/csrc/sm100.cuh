@@ -242,7 +242,7 @@ __device__ __forceinline__ void tmem_wait_st() {
 // Shared-memory matrix descriptor (sm_100 format): start address, leading and
 // stride byte offsets (16-byte units), version 1, swizzle layout type
 // (0 = none, 2 = 128-byte, 4 = 64-byte, 6 = 32-byte).
-enum : uint32_t { kSwNone = 0, kSw128 = 2, kSw64 = 4 };
+enum : uint32_t { kSwNone = 0, kSw128 = 2, kSw64 = 4, kSw32 = 6 };
 __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo_bytes,
                                               uint32_t sbo_bytes, uint32_t layout) {
     uint64_t d = 0;
@@ -278,12 +278,15 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
 }
 
 // Byte offset of 16-byte chunk `c` of row `r` in a swizzled tile whose rows are
-// 128 bytes (resp. 64 bytes); the tile base must be 1024- (resp. 512-) aligned.
+// 128 bytes (resp. 64, 32 bytes); the tile base must be 1024- (resp. 512-, 256-) aligned.
 __device__ __forceinline__ uint32_t sw128_off(uint32_t r, uint32_t c) {
     return r * 128u + (((c ^ r) & 7u) << 4);
 }
 __device__ __forceinline__ uint32_t sw64_off(uint32_t r, uint32_t c) {
     return r * 64u + (((c ^ (r >> 1)) & 3u) << 4);
+}
+__device__ __forceinline__ uint32_t sw32_off(uint32_t r, uint32_t c) {
+    return r * 32u + (((c ^ (r >> 2)) & 1u) << 4);
 }
 
 }  // namespace sm100

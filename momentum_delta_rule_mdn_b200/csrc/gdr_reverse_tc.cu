@@ -72,18 +72,18 @@ constexpr int B_FFB = 2;   // [2] images landed
 constexpr int B_FVD = 4;   // [NV] Vtilde, dO, record landed
 constexpr int B_EVD = 6;   // [NV] ... read (after A1 of the chunk, so after R)
 constexpr int B_M1 = 8;    //     A1 (and R) complete
-constexpr int B_MT = 9;    //     AT complete (the images' slot is free)
-constexpr int B_M2 = 10;   // [2] A2 complete (the K, Q slot is free)
-constexpr int B_YR = 12;   //     E' written
-constexpr int B_GR = 13;   //     -D dv written
-constexpr int B_VR = 14;   //     dv tiles written
-constexpr int B_SR = 15;   //     next adjoint written
-constexpr int B_EO = 16;   // [2] Dq dO written, rows behind the sequence cleared (two: the first two
+constexpr int B_MT = 9;    // [2] AT complete (the images' slot is free)
+constexpr int B_M2 = 11;   // [2] A2 complete (the K, Q slot is free)
+constexpr int B_YR = 13;   //     E' written
+constexpr int B_GR = 14;   //     -D dv written
+constexpr int B_VR = 15;   //     dv tiles written
+constexpr int B_SR = 16;   //     next adjoint written
+constexpr int B_EO = 17;   // [2] Dq dO written, rows behind the sequence cleared (two: the first two
                            //     chunks' are formed with nothing waited for in between)
-constexpr int B_VF = 18;   //     dv tiles stored
-constexpr int B_GF = 19;   //     the bf16 adjoint's tile has been stored
-constexpr int B_FIN = 20;
-constexpr int kBars = 21;
+constexpr int B_VF = 19;   //     dv tiles stored
+constexpr int B_GF = 20;   //     the bf16 adjoint's tile has been stored
+constexpr int B_FIN = 21;
+constexpr int kBars = 22;
 
 template <int NS>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -214,18 +214,17 @@ reverse_kernel_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
                 mma_bf16_elect(tmem + L::TM_AT, df + (kBlkTlo >> 4) + ks * (2048 >> 4), d_y + ks * (2048 >> 4), idt, 1);
-            mma_commit_elect(&bars[B_MT]);
-            // under the dv epilogue: R of the next chunk (with one slot of images, which it still
-            // waits for here, under the state's)
+            mma_commit_elect(&bars[B_MT + s2]);
             if (m + 1 < NT && !warp_wait(&bars[B_FKQ + ((m + 1) & 1)], ((m + 1) >> 1) & 1, abort_flag)) break;
-            if (L::NFB == 2 && m + 1 < NT && !rpart(m + 1)) break;
             if (!warp_wait(&bars[B_GR], m & 1, abort_flag)) break;
             tc_fence_after_sync();
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
                 mma_bf16_elect(tmem + L::TM_A2, dkt + ks * (2048 >> 4), d_y + ks * (2048 >> 4), id2, 1);
             mma_commit_elect(&bars[B_M2 + s2]);
-            if (L::NFB == 1 && m + 1 < NT && !rpart(m + 1)) break;
+            // under the state's epilogue: R of the next chunk (under that of dv its images' load is
+            // still waited for, and the wait holds up A2)
+            if (m + 1 < NT && !rpart(m + 1)) break;
         }
         mma_commit_elect(&bars[B_FIN]);
         (void)mbar_wait(&bars[B_FIN], 0);
@@ -237,8 +236,21 @@ reverse_kernel_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             for (int m = 0; m < NT; ++m) {
                 const int n = NT - 1 - m, s2 = m & 1, sv = m % NV, sf = m % L::NFB, t = tt0 + n * kChunk;
                 const uint8_t* blk = a.blk + head_chunk(n) * kBwdBytes;
+                // the images first: their slot is free before the K, Q slot is
+                if (m >= L::NFB && !wait_bar(&bars[B_MT + ((m - L::NFB) & 1)], ((m - L::NFB) >> 1) & 1, abort_flag)) break;
+                uint64_t* fb = &bars[B_FFB + sf];
+                mbar_arrive_expect_tx(fb, kBwdImg);
+                bulk_load(sm + L::FB0 + sf * kBwdImg, blk, kBwdImg, fb);
+                done_fb = m + 1;
+                if (m >= NV && !wait_bar(&bars[B_EVD + sv], ((m / NV) - 1) & 1, abort_flag)) break;
+                fb = &bars[B_FVD + sv];
+                mbar_arrive_expect_tx(fb, 2 * L::V_BYTES + kBwdRecBytes);
+                tma_load_4d(sm + L::V0 + sv * L::V_BYTES, &tm_vt, j0, ch.h, t, tb, fb);
+                tma_load_4d(sm + L::O0 + sv * L::V_BYTES, &tm_do, j0, ch.h, t, tb, fb);
+                bulk_load(sm + L::CR0 + sv * kBwdRecBytes, blk + kBwdImg, kBwdRecBytes, fb);
+                done_vd = m + 1;
                 if (m >= 2 && !wait_bar(&bars[B_M2 + s2], ((m - 2) >> 1) & 1, abort_flag)) break;
-                uint64_t* fb = &bars[B_FKQ + s2];
+                fb = &bars[B_FKQ + s2];
                 mbar_arrive_expect_tx(fb, 32768);
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
@@ -247,20 +259,6 @@ reverse_kernel_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     tma_load_4d(dst + 8192, &tm_q, q * 64, ch.hk, t, tb, fb);
                 }
                 done_kq = m + 1;
-                if (m >= NV && !wait_bar(&bars[B_EVD + sv], ((m / NV) - 1) & 1, abort_flag)) break;
-                fb = &bars[B_FVD + sv];
-                mbar_arrive_expect_tx(fb, 2 * L::V_BYTES + kBwdRecBytes);
-                tma_load_4d(sm + L::V0 + sv * L::V_BYTES, &tm_vt, j0, ch.h, t, tb, fb);
-                tma_load_4d(sm + L::O0 + sv * L::V_BYTES, &tm_do, j0, ch.h, t, tb, fb);
-                bulk_load(sm + L::CR0 + sv * kBwdRecBytes, blk + kBwdImg, kBwdRecBytes, fb);
-                done_vd = m + 1;
-                // two slots: A2 of chunk m - 2 (waited for above) followed its AT; one slot: AT of
-                // chunk m - 1, whose barrier cannot advance again before this load
-                if (L::NFB == 1 && m >= 1 && !wait_bar(&bars[B_MT], (m - 1) & 1, abort_flag)) break;
-                fb = &bars[B_FFB + sf];
-                mbar_arrive_expect_tx(fb, kBwdImg);
-                bulk_load(sm + L::FB0 + sf * kBwdImg, blk, kBwdImg, fb);
-                done_fb = m + 1;
             }
             for (int m = done_kq - 2; m < done_kq; ++m)
                 if (m >= 0) (void)mbar_wait(&bars[B_FKQ + (m & 1)], (m >> 1) & 1);
@@ -273,21 +271,27 @@ reverse_kernel_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     } else if (chain) {
         // ------------------------------------------------------------ chain epilogues
         const int r0 = quad * 16 + (lid >> 2), pc = (lid & 3) * 4;
-        for (int m = 0; m < NT; ++m) {
-            const int n = NT - 1 - m, s2 = m & 1, sv = m % NV, valid = ch.len - n * kChunk;
-            const size_t hcn = head_chunk(n);
-            // XS of this thread's rows and columns
-            float4 xs[NP];
+        // XS of this thread's rows and columns, and its part of the state entering the chunk:
+        // loaded a chunk ahead, where they are used
+        float4 xs[NP], se[NH / 4];
+        auto load_xs = [&](int n) {
 #pragma unroll
             for (int c = 0; c < NP; ++c)
                 xs[c] = *reinterpret_cast<const float4*>(
-                    a.xs + ((hcn * SL + slice) * CW + (warp - kChainWarp0)) * (NP * 128) + 128 * c + 4 * lid);
-            float4 se[NH / 4];  // the state entering the chunk
-            {
-                const float* src = a.ssf + ((hcn * SL + slice) * CW + (warp - kChainWarp0)) * (NH * 32) + 4 * lid;
+                    a.xs + ((head_chunk(n) * SL + slice) * CW + (warp - kChainWarp0)) * (NP * 128) + 128 * c + 4 * lid);
+        };
+        auto load_se = [&](int n) {
+            const float* src = a.ssf + ((head_chunk(n) * SL + slice) * CW + (warp - kChainWarp0)) * (NH * 32) + 4 * lid;
 #pragma unroll
-                for (int j = 0; j < NH / 4; ++j) se[j] = *reinterpret_cast<const float4*>(src + 128 * j);
-            }
+            for (int j = 0; j < NH / 4; ++j) se[j] = *reinterpret_cast<const float4*>(src + 128 * j);
+        };
+        if (NT > 0) {
+            load_xs(NT - 1);
+            load_se(NT - 1);
+        }
+        for (int m = 0; m < NT; ++m) {
+            const int n = NT - 1 - m, s2 = m & 1, sv = m % NV, valid = ch.len - n * kChunk;
+            const size_t hcn = head_chunk(n);
             if (!warp_wait(&bars[B_FVD + sv], (m / NV) & 1, abort_flag)) break;
             const float* cr = reinterpret_cast<const float*>(sm + L::CR0 + sv * kBwdRecBytes);
             const float aC = cr[kRecBwdB];
@@ -352,6 +356,7 @@ reverse_kernel_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 for (int j = 0; j < NH; j += 4)
                     t = fmaf(g[j], se[j / 4].x, fmaf(g[j + 1], se[j / 4].y,
                         fmaf(g[j + 2], se[j / 4].z, fmaf(g[j + 3], se[j / 4].w, t))));
+                if (n > 0) load_se(n - 1);
 #pragma unroll
                 for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
                 if (lid == 0) a.gs[(hcn * SL + slice) * CW + (warp - kChainWarp0)] = aC * t;
@@ -362,7 +367,7 @@ reverse_kernel_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             }
             // the last chunk's dv has left
             if (m >= 1 && !warp_wait(&bars[B_VF], (m - 1) & 1, abort_flag)) break;
-            if (!warp_wait(&bars[B_MT], m & 1, abort_flag)) break;
+            if (!warp_wait(&bars[B_MT + s2], (m >> 1) & 1, abort_flag)) break;
             tc_fence_after_sync();
             tmem_ld_16x256<NP>(tq + L::TM_AT + NH * hc, x);
             tmem_ld_16x256<NP>(tq + L::TM_AT + NS + NH * hc, y);
@@ -400,6 +405,7 @@ reverse_kernel_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     *reinterpret_cast<uint32_t*>(sm + L::VB + at) = hi;
                     *reinterpret_cast<uint32_t*>(sm + L::VL + at) = lo;
                 }
+            if (n > 0) load_xs(n - 1);
             fence_proxy_async_smem();
             __syncwarp();
             if (lid == 0) mbar_arrive(&bars[B_VR]);

@@ -59,9 +59,10 @@ struct Cfg {
     static constexpr int kThreads = (kOutWarp0 + OW) * 32;
     static constexpr int KP = D / 64;  // 64-column panels of K, Q
     static constexpr uint32_t KQ_BYTES = KP * 16384;
-    static constexpr uint32_t KQ0 = 0;                        // [K; Q], 2 slots
-    static constexpr uint32_t FB0 = 2 * KQ_BYTES;             // T_hi, Att, T_lo, 2 slots
-    static constexpr uint32_t ST = FB0 + 2 * kBlkImg;         // [S_hi | S_lo], D rows, MN-major
+    static constexpr int NK = NS <= 32 ? 3 : 2;               // slots of K, Q and of T, Att
+    static constexpr uint32_t KQ0 = 0;                        // [K; Q], NK slots
+    static constexpr uint32_t FB0 = NK * KQ_BYTES;            // T_hi, Att, T_lo, NK slots
+    static constexpr uint32_t ST = FB0 + NK * kBlkImg;        // [S_hi | S_lo], D rows, MN-major
     static constexpr uint32_t ST_BYTES = D * 2 * NS * 2;
     static constexpr uint32_t YB = ST + ST_BYTES;             // [Y_hi | Y_lo], then [gV_hi | gV_lo]
     static constexpr uint32_t V_BYTES = 64 * NS * 2;
@@ -70,7 +71,7 @@ struct Cfg {
     static constexpr uint32_t V0 = OB + V_BYTES;              // V slice, the same layout, NVC slots
     static constexpr uint32_t CR0 = V0 + NVC * V_BYTES;       // records
     static constexpr uint32_t BARS = CR0 + NVC * 1024;
-    static constexpr uint32_t MISC = BARS + 256;
+    static constexpr uint32_t MISC = BARS + 288;
     static constexpr uint32_t BYTES = MISC + 16;
     static_assert(BYTES <= 232448, "shared memory");
     static constexpr uint32_t TM_KS = 0;             // 2 NS
@@ -95,22 +96,24 @@ struct Cfg {
 };
 
 // mbarriers
-constexpr int B_FKQ = 0;   // [2] K, Q landed
-constexpr int B_FFB = 2;   // [2] T, Att landed
-constexpr int B_FVC = 4;   // [4] V, record landed
-constexpr int B_EVC = 8;   // [4] V, record slot read (chain and output warps)
-constexpr int B_M1 = 12;   //     A1 complete
-constexpr int B_MT = 13;   //     AT complete
-constexpr int B_M2 = 14;   // [2] A2 complete (and A1, QS: the K, Q slot is free)
-constexpr int B_MO = 16;   // [2] AO complete (the T, Att slot is free)
-constexpr int B_YR = 18;   //     Y written
-constexpr int B_GR = 19;   //     gam Vtilde written
-constexpr int B_VR = 20;   //     Vtilde written
-constexpr int B_SR = 21;   //     next state written
-constexpr int B_OD = 22;   // [2] QS, AO slot read by the output warps
-constexpr int B_VF = 24;   //     Vtilde stored: its tile is free
-constexpr int B_FIN = 25;
-constexpr int kBars = 26;
+constexpr int B_FKQ = 0;   // [3] K, Q landed
+constexpr int B_FFB = 3;   // [3] T, Att landed
+constexpr int B_KF = 6;    // [3] K, Q slot free (A2 complete, and A1, QS before it)
+constexpr int B_FF = 9;    // [3] T, Att slot free (AO complete)
+constexpr int B_FVC = 12;  // [4] V, record landed
+constexpr int B_EVC = 16;  // [4] V, record slot read (chain and output warps)
+constexpr int B_M1 = 20;   //     A1 complete
+constexpr int B_MT = 21;   //     AT complete
+constexpr int B_M2 = 22;   // [2] A2 complete
+constexpr int B_MO = 24;   // [2] AO complete
+constexpr int B_YR = 26;   //     Y written
+constexpr int B_GR = 27;   //     gam Vtilde written
+constexpr int B_VR = 28;   //     Vtilde written
+constexpr int B_SR = 29;   //     next state written
+constexpr int B_OD = 30;   // [2] QS, AO slot read by the output warps
+constexpr int B_VF = 32;   //     Vtilde stored: its tile is free
+constexpr int B_FIN = 33;
+constexpr int kBars = 34;
 
 struct ChainArgs {
     Args a;
@@ -131,7 +134,7 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
 {
     using L = Cfg<D, NS>;
     constexpr int NH = L::NH, NP = NH / 8;  // NP: 8-column pieces of a chain thread
-    constexpr int CW = L::CW, kOutWarp0 = L::kOutWarp0;
+    constexpr int CW = L::CW, kOutWarp0 = L::kOutWarp0, NK = L::NK;
     const Args& a = p.a;
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sbase = smem_u32(sm);
@@ -217,8 +220,9 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             const int s2 = n & 1;
             if (n >= 1 && !warp_wait(&bars[B_SR], (n - 1) & 1, abort_flag)) break;
             tc_fence_after_sync();
-            const uint64_t dk = d_k0 + s2 * (L::KQ_BYTES >> 4), dq = dk + (8192 >> 4);
-            const uint64_t dfb = d_fb0 + s2 * (kBlkImg >> 4);
+            const int sk = n % NK;
+            const uint64_t dk = d_k0 + sk * (L::KQ_BYTES >> 4), dq = dk + (8192 >> 4);
+            const uint64_t dfb = d_fb0 + sk * (kBlkImg >> 4);
             const uint32_t qs = tmem + L::TM_QS + NS * s2;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
@@ -229,7 +233,7 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             for (int ks = 0; ks < KS / 2; ++ks)
                 mma_bf16_elect(qs, dq + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
                                d_st + ks * ystep, ido, ks > 0);
-            if (!warp_wait(&bars[B_FFB + s2], (n >> 1) & 1, abort_flag)) break;
+            if (!warp_wait(&bars[B_FFB + sk], (n / NK) & 1, abort_flag)) break;
             if (!warp_wait(&bars[B_YR], n & 1, abort_flag)) break;
             tc_fence_after_sync();
 #pragma unroll
@@ -244,15 +248,16 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 mma_bf16_elect(qs, dq + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
                                d_st + ks * ystep, ido, 1);
             // what the next chunk's products need, while Vtilde is formed
-            if (n + 1 < NT && !warp_wait(&bars[B_FKQ + ((n + 1) & 1)], ((n + 1) >> 1) & 1, abort_flag)) break;
+            if (n + 1 < NT && !warp_wait(&bars[B_FKQ + (n + 1) % NK], ((n + 1) / NK) & 1, abort_flag)) break;
             if (n >= 1 && !warp_wait(&bars[B_OD + ((n + 1) & 1)], ((n - 1) >> 1) & 1, abort_flag)) break;
             if (!warp_wait(&bars[B_GR], n & 1, abort_flag)) break;
             tc_fence_after_sync();
-            const uint64_t dkt = d_kt0 + s2 * (L::KQ_BYTES >> 4);
+            const uint64_t dkt = d_kt0 + sk * (L::KQ_BYTES >> 4);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
                 mma_bf16_elect(tmem + L::TM_A2, dkt + ks * (2048 >> 4), d_y + ks * ystep, id2, ks > 0);
             mma_commit_elect(&bars[B_M2 + s2]);
+            mma_commit_elect(&bars[B_KF + sk]);
             if (!warp_wait(&bars[B_VR], n & 1, abort_flag)) break;
             tc_fence_after_sync();
 #pragma unroll
@@ -260,6 +265,7 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 mma_bf16_elect(tmem + L::TM_AO + NS * s2, dfb + (kBlkAtt >> 4) + ks * 2, d_v + ks * vstep,
                                ido, ks > 0);
             mma_commit_elect(&bars[B_MO + s2]);
+            mma_commit_elect(&bars[B_FF + sk]);
         }
         mma_commit_elect(&bars[B_FIN]);
         (void)mbar_wait(&bars[B_FIN], 0);
@@ -269,15 +275,15 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         if (lid == 0) {
             int done_kq = 0, done_fb = 0, done_vc = 0;
             for (int n = 0; n < NT; ++n) {
-                const int s2 = n & 1, sv = n % NVC;
+                const int sk = n % NK, sv = n % NVC;
                 const size_t blk = (size_t)((ch.chunk0 + n) * a.H + ch.h) * kBlkBytes;
                 const int t = tt0 + n * kChunk;
-                if (n >= 2 && !wait_bar(&bars[B_M2 + s2], ((n - 2) >> 1) & 1, abort_flag)) break;
-                uint64_t* fb = &bars[B_FKQ + s2];
+                if (n >= NK && !wait_bar(&bars[B_KF + sk], ((n / NK) - 1) & 1, abort_flag)) break;
+                uint64_t* fb = &bars[B_FKQ + sk];
                 mbar_arrive_expect_tx(fb, L::KQ_BYTES);
 #pragma unroll
                 for (int q = 0; q < L::KP; ++q) {
-                    uint8_t* dst = sm + L::KQ0 + s2 * L::KQ_BYTES + q * 16384;
+                    uint8_t* dst = sm + L::KQ0 + sk * L::KQ_BYTES + q * 16384;
                     tma_load_4d(dst, &tm_k, q * 64, ch.hk, t, tb, fb);
                     tma_load_4d(dst + 8192, &tm_q, q * 64, ch.hk, t, tb, fb);
                 }
@@ -288,17 +294,17 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 tma_load_4d(sm + L::V0 + sv * L::V_BYTES, &tm_v, j0, ch.h, t, tb, fb);
                 bulk_load(sm + L::CR0 + sv * 1024, p.blk + blk + kBlkRec, 1024, fb);
                 done_vc = n + 1;
-                if (n >= 2 && !wait_bar(&bars[B_MO + s2], ((n - 2) >> 1) & 1, abort_flag)) break;
-                fb = &bars[B_FFB + s2];
+                if (n >= NK && !wait_bar(&bars[B_FF + sk], ((n / NK) - 1) & 1, abort_flag)) break;
+                fb = &bars[B_FFB + sk];
                 mbar_arrive_expect_tx(fb, kBlkImg);
-                bulk_load(sm + L::FB0 + s2 * kBlkImg, p.blk + blk, kBlkImg, fb);
+                bulk_load(sm + L::FB0 + sk * kBlkImg, p.blk + blk, kBlkImg, fb);
                 done_fb = n + 1;
             }
             // copies in flight must land before shared memory is released
-            for (int n = done_kq - 2; n < done_kq; ++n)
-                if (n >= 0) (void)mbar_wait(&bars[B_FKQ + (n & 1)], (n >> 1) & 1);
-            for (int n = done_fb - 2; n < done_fb; ++n)
-                if (n >= 0) (void)mbar_wait(&bars[B_FFB + (n & 1)], (n >> 1) & 1);
+            for (int n = done_kq - NK; n < done_kq; ++n)
+                if (n >= 0) (void)mbar_wait(&bars[B_FKQ + n % NK], (n / NK) & 1);
+            for (int n = done_fb - NK; n < done_fb; ++n)
+                if (n >= 0) (void)mbar_wait(&bars[B_FFB + n % NK], (n / NK) & 1);
             for (int n = done_vc - NVC; n < done_vc; ++n)
                 if (n >= 0) (void)mbar_wait(&bars[B_FVC + n % NVC], (n / NVC) & 1);
         }
@@ -328,11 +334,11 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             if (valid < kChunk && a.cu_s) {
                 // K rows behind the sequence belong to the next one (or to none) and
                 // may hold anything: they meet zeros in A2, so make them zero
-                if (!warp_wait(&bars[B_FKQ + s2], (n >> 1) & 1, abort_flag)) break;
+                if (!warp_wait(&bars[B_FKQ + n % NK], (n / NK) & 1, abort_flag)) break;
                 for (int e = (warp - kChainWarp0) * 32 + lid; e < 64 * 8 * L::KP; e += CW * 32) {
                     const int r = e / (8 * L::KP), q = e % (8 * L::KP);
                     if (r >= valid)
-                        *reinterpret_cast<uint4*>(sm + L::KQ0 + s2 * L::KQ_BYTES + (q >> 3) * 16384 +
+                        *reinterpret_cast<uint4*>(sm + L::KQ0 + (n % NK) * L::KQ_BYTES + (q >> 3) * 16384 +
                                                   sw128_off(r, q & 7)) = make_uint4(0, 0, 0, 0);
                 }
             }

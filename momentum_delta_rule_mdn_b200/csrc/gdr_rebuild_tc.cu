@@ -34,8 +34,9 @@ template <int NS>
 struct Cfg {
     static constexpr int NH = NS / 4;
     static constexpr int NV = NS == 32 ? 4 : 2;              // slots of Vtilde, dO and the record
-    static constexpr uint32_t KQ0 = 0;                       // [K; Q], 2 slots
-    static constexpr uint32_t ST0 = 2 * 32768;               // [S_hi | S_lo], 2 slots
+    static constexpr int NK = NS == 32 ? 3 : 2;              // slots of K, Q
+    static constexpr uint32_t KQ0 = 0;                       // [K; Q], NK slots
+    static constexpr uint32_t ST0 = NK * 32768;              // [S_hi | S_lo], 2 slots
     static constexpr uint32_t ST_BYTES = D * 2 * NS * 2;
     static constexpr uint32_t SI = ST0 + 2 * ST_BYTES;       // the entering state in bf16, to be stored
     static constexpr uint32_t GV0 = SI + D * NS * 2;         // [gV_hi | gV_lo], 2 slots
@@ -59,17 +60,18 @@ struct Cfg {
     }
 };
 
-constexpr int B_FKQ = 0;   // [2] K, Q landed
-constexpr int B_FVD = 2;   // [4] Vtilde, dO, record landed
-constexpr int B_EVD = 6;   // [4] ... read
-constexpr int B_M1 = 10;   // [2] A1 complete
-constexpr int B_M2 = 12;   // [2] A2 complete (and the A1 before it)
-constexpr int B_GV = 14;   // [2] gV written
-constexpr int B_SR = 16;   // [2] next state written
-constexpr int B_OD = 18;   //     A1 read
-constexpr int B_SF = 19;   //     the bf16 state's tile has been stored
-constexpr int B_FIN = 20;
-constexpr int kBars = 21;
+constexpr int B_FKQ = 0;   // [3] K, Q landed
+constexpr int B_FVD = 3;   // [4] Vtilde, dO, record landed
+constexpr int B_EVD = 7;   // [4] ... read
+constexpr int B_M1 = 11;   // [2] A1 complete
+constexpr int B_M2 = 13;   // [2] A2 complete (and the A1 before it)
+constexpr int B_GV = 15;   // [2] gV written
+constexpr int B_SR = 17;   // [2] next state written
+constexpr int B_OD = 19;   //     A1 read
+constexpr int B_SF = 20;   //     the bf16 state's tile has been stored
+constexpr int B_KF = 21;   // [3] K, Q slot free (A1 complete, and the A2 before it)
+constexpr int B_FIN = 24;
+constexpr int kBars = 25;
 
 template <int NS>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -78,7 +80,7 @@ rebuild_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                const __grid_constant__ CUtensorMap tm_sb, const Args a)
 {
     using L = Cfg<NS>;
-    constexpr int NH = L::NH, NP = NH / 8, SL = D / NS, NV = L::NV;
+    constexpr int NH = L::NH, NP = NH / 8, SL = D / NS, NV = L::NV, NK = L::NK;
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sbase = smem_u32(sm);
     const int tid = threadIdx.x, lid = tid & 31;
@@ -157,11 +159,11 @@ rebuild_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         constexpr uint32_t id1 = idesc_bf16(64, 2 * NS, false, true);
         constexpr uint32_t id2 = idesc_bf16(128, 2 * NS, true, true);
         auto update = [&](int n) {  // A2 of chunk n; its TMEM slot was read before SR of n - 2
-            const int s2 = n & 1;
-            if (!warp_wait(&bars[B_FKQ + s2], (n >> 1) & 1, abort_flag)) return false;
+            const int s2 = n & 1, sk = n % NK;
+            if (!warp_wait(&bars[B_FKQ + sk], (n / NK) & 1, abort_flag)) return false;
             if (!warp_wait(&bars[B_GV + s2], (n >> 1) & 1, abort_flag)) return false;
             tc_fence_after_sync();
-            const uint64_t dkt = d_kt0 + s2 * (32768 >> 4), dgv = d_gv0 + s2 * (L::GV_BYTES >> 4);
+            const uint64_t dkt = d_kt0 + sk * (32768 >> 4), dgv = d_gv0 + s2 * (L::GV_BYTES >> 4);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
                 mma_bf16_elect(tmem + L::TM_A2 + 2 * NS * s2, dkt + ks * (2048 >> 4), dgv + ks * (2048 >> 4),
@@ -175,7 +177,7 @@ rebuild_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             if (n >= 1 && !warp_wait(&bars[B_SR + (s2 ^ 1)], ((n - 1) >> 1) & 1, abort_flag)) break;
             if (n >= 1 && !warp_wait(&bars[B_OD], (n - 1) & 1, abort_flag)) break;
             tc_fence_after_sync();
-            const uint64_t dk = d_k0 + s2 * (32768 >> 4), dst = d_st0 + s2 * (L::ST_BYTES >> 4);
+            const uint64_t dk = d_k0 + (n % NK) * (32768 >> 4), dst = d_st0 + s2 * (L::ST_BYTES >> 4);
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
                 const uint64_t d = dk + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4);
@@ -183,6 +185,7 @@ rebuild_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 mma_bf16_elect(tmem + L::TM_A1 + 2 * NS, d + (8192 >> 4), dst + ks * (2048 >> 4), id1, ks > 0);
             }
             mma_commit_elect(&bars[B_M1 + s2]);
+            mma_commit_elect(&bars[B_KF + n % NK]);
             // the next update needs no state; the state it follows is one epilogue away
             if (n + 1 < NT && !update(n + 1)) break;
         }
@@ -194,28 +197,28 @@ rebuild_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         if (lid == 0) {
             int done_kq = 0, done_vd = 0;
             for (int n = 0; n < NT; ++n) {
-                const int s2 = n & 1, sv = n % NV, t = tt0 + n * kChunk;
-                if (n >= 2 && !wait_bar(&bars[B_M1 + s2], ((n - 2) >> 1) & 1, abort_flag)) break;  // A2 came before
-                uint64_t* fb = &bars[B_FKQ + s2];
-                mbar_arrive_expect_tx(fb, 32768);
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint8_t* dst = sm + L::KQ0 + s2 * 32768 + q * 16384;
-                    tma_load_4d(dst, &tm_k, q * 64, ch.hk, t, tb, fb);
-                    tma_load_4d(dst + 8192, &tm_q, q * 64, ch.hk, t, tb, fb);
-                }
-                done_kq = n + 1;
+                const int sk = n % NK, sv = n % NV, t = tt0 + n * kChunk;
                 if (n >= NV && !wait_bar(&bars[B_EVD + sv], ((n / NV) - 1) & 1, abort_flag)) break;
-                fb = &bars[B_FVD + sv];
+                uint64_t* fb = &bars[B_FVD + sv];
                 mbar_arrive_expect_tx(fb, 2 * L::V_BYTES + kBwdRecBytes);
                 tma_load_4d(sm + L::V0 + sv * L::V_BYTES, &tm_vt, j0, ch.h, t, tb, fb);
                 tma_load_4d(sm + L::O0 + sv * L::V_BYTES, &tm_do, j0, ch.h, t, tb, fb);
                 bulk_load(sm + L::CR0 + sv * kBwdRecBytes, a.blk + head_chunk(n) * kBwdBytes + kBwdImg,
                           kBwdRecBytes, fb);
                 done_vd = n + 1;
+                if (n >= NK && !wait_bar(&bars[B_KF + sk], ((n / NK) - 1) & 1, abort_flag)) break;
+                fb = &bars[B_FKQ + sk];
+                mbar_arrive_expect_tx(fb, 32768);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint8_t* dst = sm + L::KQ0 + sk * 32768 + q * 16384;
+                    tma_load_4d(dst, &tm_k, q * 64, ch.hk, t, tb, fb);
+                    tma_load_4d(dst + 8192, &tm_q, q * 64, ch.hk, t, tb, fb);
+                }
+                done_kq = n + 1;
             }
-            for (int n = done_kq - 2; n < done_kq; ++n)
-                if (n >= 0) (void)mbar_wait(&bars[B_FKQ + (n & 1)], (n >> 1) & 1);
+            for (int n = done_kq - NK; n < done_kq; ++n)
+                if (n >= 0) (void)mbar_wait(&bars[B_FKQ + n % NK], (n / NK) & 1);
             for (int n = done_vd - NV; n < done_vd; ++n)
                 if (n >= 0) (void)mbar_wait(&bars[B_FVD + n % NV], (n / NV) & 1);
         }
@@ -332,11 +335,11 @@ rebuild_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
             if (valid < kChunk && a.cu_s) {
                 // K rows behind the sequence may hold anything: zeros, as in the forward chain
-                if (!warp_wait(&bars[B_FKQ + s2], (n >> 1) & 1, abort_flag)) break;
+                if (!warp_wait(&bars[B_FKQ + n % NK], (n / NK) & 1, abort_flag)) break;
                 for (int e = ot; e < 64 * 16; e += AW * 32) {
                     const int rr = e >> 4, q = e & 15;
                     if (rr >= valid)
-                        *reinterpret_cast<uint4*>(sm + L::KQ0 + s2 * 32768 + (q >> 3) * 16384 + sw128_off(rr, q & 7)) =
+                        *reinterpret_cast<uint4*>(sm + L::KQ0 + (n % NK) * 32768 + (q >> 3) * 16384 + sw128_off(rr, q & 7)) =
                             make_uint4(0, 0, 0, 0);
                 }
             }

@@ -48,7 +48,7 @@ mdn_status check_sizes(const Sizes& z)
 }
 
 struct Layout {
-    size_t status, cu_s, cu_c, seq_order, chunk_order;
+    size_t status, head, cu_s, cu_c, seq_order, chunk_order;
     size_t blk;                    // forward on the tensor cores
     size_t SS, GG, dvf, dqp, dkp;  // backward on CUDA cores
     size_t ssf, sb, gb, xs, po, px, pb, pw, gs, dvl;  // backward on the tensor cores
@@ -59,7 +59,12 @@ struct Layout {
 Layout layout(const Sizes& z, bool bwd)
 {
     Layout w = {};
-    size_t off = align_up(64);  // status words first: mdn_chunk_fwd_status reads them there
+    // status words first (mdn_chunk_fwd_status reads them there), then the ready flags and the
+    // work counter of the operand blocks: one memset clears both
+    size_t off = 64;
+    if (z.tc()) off += ((size_t)z.chunks() * z.H + 2) * sizeof(unsigned);
+    w.head = off;
+    off = align_up(off);
     if (z.packed) {
         w.cu_s = off;        off += align_up((size_t)(z.B + 1) * sizeof(int));
         w.cu_c = off;        off += align_up((size_t)(z.B + 1) * sizeof(int));
@@ -113,7 +118,8 @@ mdn_status begin(gdr::Args& a, const Sizes& z, const Layout& w, char* ws, const 
     a.B = z.B; a.T = z.T; a.Hk = z.Hk; a.H = z.H; a.D = z.dk;
     a.NT = (int)(z.packed ? z.chunks() : ((long long)z.T + z.C - 1) / z.C);
     a.status = reinterpret_cast<unsigned*>(ws + w.status);
-    cudaError_t e = cudaMemsetAsync(a.status, 0, 64, s);
+    if (z.tc()) a.ready = a.status + 16;
+    cudaError_t e = cudaMemsetAsync(a.status, 0, w.head, s);
     if (e != cudaSuccess) return cuda_fail(e);
     if (!z.packed) return MDN_OK;
     int* cu_s = reinterpret_cast<int*>(ws + w.cu_s);

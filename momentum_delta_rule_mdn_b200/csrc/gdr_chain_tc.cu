@@ -37,6 +37,8 @@
 // warps (warp w: lane quadrant w % 4, one of four column groups) hold the state;
 // 4 output warps.  Every wait is bounded as in the inter-chunk kernels of the
 // momentum rule.
+#include <cmath>
+
 #include "gdr_tc.cuh"
 
 namespace mdn {
@@ -118,6 +120,7 @@ constexpr int kBars = 34;
 struct ChainArgs {
     Args a;
     const uint8_t* blk;
+    bool overlap;  // the operand kernel may still be running: wait for each block's flag
 };
 
 template <int N>
@@ -289,6 +292,11 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 }
                 done_kq = n + 1;
                 if (n >= NVC && !wait_bar(&bars[B_EVC + sv], ((n / NVC) - 1) & 1, abort_flag)) break;
+                // the chunk's block is in global memory (its kernel may still be running)
+                if (p.overlap) {
+                    if (!inter::wait_ready(a.ready + (ch.chunk0 + n) * a.H + ch.h, abort_flag)) break;
+                    fence_proxy_async_global();
+                }
                 fb = &bars[B_FVC + sv];
                 mbar_arrive_expect_tx(fb, L::V_BYTES + 1024);
                 tma_load_4d(sm + L::V0 + sv * L::V_BYTES, &tm_v, j0, ch.h, t, tb, fb);
@@ -480,6 +488,8 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         if (lid == 0) bulk_wait_group_all();
     }
 
+    // a call that follows may clear the work counter: not before the operand kernel is done
+    if (p.overlap) pdl_wait();
     tc_fence_before_sync();
     __syncthreads();
     const bool ok = *abort_flag == 0;
@@ -496,7 +506,7 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
 }
 
 template <int D, int NS>
-cudaError_t launch_chain(const Args& a, cudaStream_t s)
+cudaError_t launch_chain(const Args& a, bool overlap, cudaStream_t s)
 {
     using L = Cfg<D, NS>;
     CUtensorMap mq, mk, mv, mo, mvt;
@@ -512,31 +522,71 @@ cudaError_t launch_chain(const Args& a, cudaStream_t s)
     cudaError_t e = cudaFuncSetAttribute(chain_kernel<D, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)L::BYTES);
     if (e != cudaSuccess) return e;
-    ChainArgs p{a, a.blk};
+    ChainArgs p{a, a.blk, overlap};
     ProfScope ps(kGdrChain, s);
-    chain_kernel<D, NS><<<(unsigned)(chains(a) * (D / NS)), L::kThreads, L::BYTES, s>>>(mq, mk, mv, mo, mvt, p);
-    return cudaGetLastError();
+    if (!overlap) {
+        chain_kernel<D, NS><<<(unsigned)(chains(a) * (D / NS)), L::kThreads, L::BYTES, s>>>(mq, mk, mv, mo, mvt, p);
+        return cudaGetLastError();
+    }
+    return launch_dependent(chain_kernel<D, NS>, (unsigned)(chains(a) * (D / NS)), L::kThreads, (size_t)L::BYTES, s,
+                            mq, mk, mv, mo, mvt, p);
 }
 
 }  // namespace
 
-// Chain width.  A chunk's step takes about 2.1k, 2.8k and 4.6k cycles with 16, 32 and
-// 64 columns per CTA: the narrowest slice whose CTAs all fit on the SMs at once has the
-// shortest chain; beyond that the widest, which takes the least SM time per chunk of a
-// head (FIGURES).  Packed sequences start longest first (the longest chain is the
+// Chain width.  A chunk's step takes 1.23, 1.65 and 2.4 us with 16, 32 and 64 columns per
+// CTA (measured, 4096 tokens): the narrowest slice whose CTAs all fit on the SMs at once
+// has the shortest chain; beyond that the widest, which takes the least SM time per chunk
+// of a head of d 128 (4.8 us against 6.6 and 9.8).  16384 tokens of 16 heads: 287 us in
+// slices of 16, 374 of 32, 447 of 64.  Packed sequences start longest first (the longest chain is the
 // critical path), so they keep 32 columns up to four waves.
+//
+// The chain is launched as the operand kernel's programmatic dependent.  Its CTAs need
+// a whole SM, so the operand CTAs on as many SMs as there are chain CTAs stop after L
+// chunks each, and those on the other SMs (U of them) make the rest, which the work
+// order makes the chunks the chains need last.  With r chain steps per operand chunk
+// (11k cycles at three CTAs an SM), L minimises  L r + max(NT, rest / U r + 1).  Measured,
+// operands and chain: 16384 tokens of 16 heads 350 -> 308 us, packed sequences of 1 to
+// 24576 tokens 792 -> 683 us, 4 x 2048 tokens of 8 heads 84 -> 77 us.  More chain CTAs
+// than SMs: nothing is reserved and nothing overlaps (in 8 x 4096 tokens of 16 heads the
+// flags cost 4% and the chain gained nothing).
 cudaError_t launch_fwd_tc(const Args& a, cudaStream_t s)
 {
-    cudaError_t e = launch_operands_tc(a, s, false);
-    if (e != cudaSuccess) return e;
     int dev = 0, sms = 148;
+    cudaError_t e;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess ||
         (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
         return e;
     const long long n = chains(a);
-    if (a.D == 64) return n * 4 <= sms ? launch_chain<64, 16>(a, s) : launch_chain<64, 32>(a, s);
-    if (n * 8 <= sms) return launch_chain<128, 16>(a, s);
-    return n * 4 <= (a.cu_s ? 4 * sms : sms) ? launch_chain<128, 32>(a, s) : launch_chain<128, 64>(a, s);
+    const int ns = a.D == 64 ? (n * 4 <= sms ? 16 : 32)
+                   : n * 8 <= sms ? 16
+                   : n * 4 <= (a.cu_s ? 4 * sms : sms) ? 32 : 64;
+    const long long ctas = n * (a.D / ns);
+    int reserve = 0, limit = 1;
+    if (a.cu_s) {
+        // packed: SMs from the start for the chains of the longest sequence
+        const long long first = (long long)a.H * (a.D / ns), room = sms - sms / 4;
+        reserve = (int)(first < ctas ? (first < room ? first : room) : (ctas < room ? ctas : room));
+    } else if (ctas < sms) {
+        const double r = ns == 16 ? 5.0 : ns == 32 ? 3.9 : 2.5;
+        const long long U = 3LL * (sms - ctas), round = 3LL * sms, total = chunks(a) * a.H;
+        double best = 0.0;
+        for (int L = 1; (L - 1) * round < total; ++L) {
+            const long long rest = total - L * round;
+            const double t = L * r + (rest > 0 ? fmax((double)a.NT, (double)rest / U * r + 1.0) : (double)a.NT);
+            if (L == 1 || t < best) {
+                best = t;
+                reserve = (int)ctas;
+                limit = L;
+            }
+        }
+    }
+    if ((e = launch_operands_tc(a, s, false, reserve, limit)) != cudaSuccess) return e;
+    const bool over = reserve > 0;
+    if (a.D == 64) return ns == 16 ? launch_chain<64, 16>(a, over, s) : launch_chain<64, 32>(a, over, s);
+    return ns == 16   ? launch_chain<128, 16>(a, over, s)
+           : ns == 32 ? launch_chain<128, 32>(a, over, s)
+                      : launch_chain<128, 64>(a, over, s);
 }
 
 }  // namespace gdr

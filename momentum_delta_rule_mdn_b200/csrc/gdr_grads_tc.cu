@@ -449,7 +449,7 @@ cudaError_t launch_reverse_tc(const Args& a, int ns, cudaStream_t s);
 cudaError_t launch_bwd_tc(const Args& a, cudaStream_t s)
 {
     cudaError_t e;
-    if ((e = launch_operands_tc(a, s, true)) != cudaSuccess) return e;
+    if ((e = launch_operands_tc(a, s, true, 0, 0)) != cudaSuccess) return e;
     if ((e = launch_rebuild_tc(a, a.ns, s)) != cudaSuccess) return e;
     if ((e = launch_reverse_tc(a, a.ns, s)) != cudaSuccess) return e;
     const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;

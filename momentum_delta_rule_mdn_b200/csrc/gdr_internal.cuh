@@ -45,6 +45,8 @@ struct Args {
     const int* seq_order = nullptr;
     const int* chunk_order = nullptr;
     uint8_t* blk = nullptr;  // tensor-core path: operand blocks of every chunk and head
+    unsigned* ready = nullptr;  // [chunks * H] block written, then the work counter and the number of
+                                // operand CTAs without a limit; zeroed per call
     // backward
     const void* d_o = nullptr;
     const float* dS_T = nullptr;

@@ -7,13 +7,14 @@
 //   2  TMEM lane r is row r of A (lanes 0..63) or of Att (lanes 64..127).  Warp w < 2
 //      writes rows 32 w .. of A to shared memory in fp32 and, alone, inverts
 //      its two 16 x 16 diagonal blocks (a lane per column, forward substitution
-//      with x in registers) and joins them, T_10 = -T_11 A_10 T_00; warps 2 and 3
+//      in fp32 with x in registers) and joins them, T_10 = -T_11 A_10 T_00; warps 2 and 3
 //      write Att to the block image and scan the next chunk's gates meanwhile
-//   3  the join of the two 32 x 32 halves, by all four warps, in fp32
+//   3  the join of the two 32 x 32 halves, by all four warps
 //   4  T rounded to two bf16 terms into the image; one bulk store
 //
-// Bound by the latency of these phases (about 1.2k cycles of issue per chunk
-// and SM); three CTAs per SM is what shared memory admits.
+// Bound by the latency of these phases: 11k cycles per chunk with three CTAs per SM,
+// which is what shared memory admits; 8 x 4096 tokens of 16 heads take 107 us, of which
+// their 482 MB of inputs and blocks need 75 at the copy rate.
 //
 // The decays L need care: differences of long sums of alpha_log lose the
 // digits that exp then needs.  Inside a 16 x 16 diagonal block they are
@@ -49,7 +50,7 @@ struct Lay {
     static constexpr uint32_t BTOT = VEC + 4 * 256;          // [2][4] exp of a block's sum
     static constexpr uint32_t BARS = BTOT + 32;
     static constexpr uint32_t MISC = BARS + 16;
-    static constexpr uint32_t BYTES = MISC + 16;
+    static constexpr uint32_t BYTES = MISC + 32;
     static_assert(BARS % 8 == 0 && AM % 16 == 0, "alignment");
     static_assert(CTAS * (BYTES + 1024) <= 233472, "CTAs per SM");
 };
@@ -58,7 +59,9 @@ struct OpArgs {
     Args a;
     uint8_t* blk;
     const int* chunk_order;
+    unsigned* ready;
     int total;  // chunk-heads
+    int reserve, limit;
 };
 
 // A chunk-head of the work order: the first chunks of every chain come first.
@@ -90,33 +93,54 @@ __device__ __forceinline__ Item item(const OpArgs& o, int i)
     return x;
 }
 
-// acc (2 rows x 4 columns) += sign * X[rows] Y[:, cols] over k in [k0, k1): X rows at x, x + LDA,
-// Y rows at y; both fp32 with leading dimension LDA.
-template <bool NEG>
-__device__ __forceinline__ void tile_mm(float (&acc)[2][4], const float* x, const float* y, int k0, int k1)
+// 16 x 16 products of fp32 matrices in shared memory (leading dimension LDA), one warp:
+// the 16-row blocks are below tcgen05's smallest M, so they take the warp-level bf16
+// instruction, each factor as two bf16 terms and three of the four term products
+// (2^-16 relative, below the rounding of T to two terms).  In FP32 multiply-adds these
+// joins were half of the kernel's instructions.
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-#pragma unroll 4
-    for (int k = k0; k < k1; k += 4) {
-        const float4 x0 = lds4(x + k), x1 = lds4(x + LDA + k);
-        const float xa[4] = {x0.x, x0.y, x0.z, x0.w}, xb[4] = {x1.x, x1.y, x1.z, x1.w};
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// acc[n] (columns 8 n ..) += X (16 x 16 at x) Y (16 x 16 at y)
+__device__ __forceinline__ void block_mm(float (&acc)[2][4], const float* x, const float* y, int lane)
+{
+    const int g = lane >> 2, t = lane & 3;
+    uint32_t ah[4], al[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float4 v = lds4(y + (k + e) * LDA);
-            const float a0 = NEG ? -xa[e] : xa[e], a1 = NEG ? -xb[e] : xb[e];
-            acc[0][0] = fmaf(a0, v.x, acc[0][0]); acc[0][1] = fmaf(a0, v.y, acc[0][1]);
-            acc[0][2] = fmaf(a0, v.z, acc[0][2]); acc[0][3] = fmaf(a0, v.w, acc[0][3]);
-            acc[1][0] = fmaf(a1, v.x, acc[1][0]); acc[1][1] = fmaf(a1, v.y, acc[1][1]);
-            acc[1][2] = fmaf(a1, v.z, acc[1][2]); acc[1][3] = fmaf(a1, v.w, acc[1][3]);
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = *reinterpret_cast<const float2*>(x + (g + 8 * (i & 1)) * LDA + 2 * t + 8 * (i >> 1));
+        split2(v.x, v.y, ah[i], al[i]);
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        uint32_t bh[2], bl[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float* p = y + (2 * t + 8 * i) * LDA + 8 * n + g;
+            split2(p[0], p[LDA], bh[i], bl[i]);
         }
+        mma_16816(acc[n], ah, bh[0], bh[1]);
+        mma_16816(acc[n], ah, bl[0], bl[1]);
+        mma_16816(acc[n], al, bh[0], bh[1]);
     }
 }
-__device__ __forceinline__ void tile_st(float* dst, const float (&acc)[2][4])
+// dst (16 x 16) = f acc
+__device__ __forceinline__ void block_st(float* dst, const float (&acc)[2][4], float f, int lane)
 {
+    const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-        *reinterpret_cast<float4*>(dst + j * LDA) = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<float2*>(dst + (g + 8 * h) * LDA + 8 * n + 2 * t) =
+                make_float2(f * acc[n][2 * h], f * acc[n][2 * h + 1]);
 }
-__device__ __forceinline__ void tile_zero(float (&acc)[2][4])
+__device__ __forceinline__ void block_zero(float (&acc)[2][4])
 {
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j >> 2][j & 3] = 0.f;
@@ -133,11 +157,13 @@ operands_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sbase = smem_u32(sm);
     const int tid = threadIdx.x, lane = tid & 31;
+    pdl_launch_dependents();
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BARS);  // [0] load, [1] product
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::MISC + 4);
     float* Am = reinterpret_cast<float*>(sm + L::AM);
+    int* slot = reinterpret_cast<int*>(sm + L::MISC + 8);  // [4] work items of iterations k, k + 1, ...
     auto vec = [&](int k) { return k & 1 ? GateVec{sm + L::AM + 256, LDA * 4} : GateVec{sm + L::VEC, 16}; };
     auto btot = [&](int k) { return reinterpret_cast<float*>(sm + L::BTOT) + 4 * (k & 1); };
 
@@ -181,13 +207,29 @@ operands_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     auto rec_of = [&](const Item& x) {
         return reinterpret_cast<float*>(o.blk + ((size_t)x.n * a.H + x.h) * kBlock + L::IMG_BYTES);
     };
+    // Work items come from a counter, one thread (tid 96) taking each two iterations ahead.
     // Chunks with no tokens (a packed call's bound on its chunks) end the work order.
-    const int step = gridDim.x;
-    int i = blockIdx.x;
+    int taken = 0, limit = 1 << 30;
+    auto take = [&]() -> int {
+        // stop at the limit, provided that a CTA without one is at work on the rest
+        if (taken >= limit && *reinterpret_cast<volatile unsigned*>(o.ready + o.total + 1)) return o.total;
+        ++taken;
+        const unsigned c = atomicAdd(o.ready + o.total, 1u);
+        return c < (unsigned)o.total ? (int)c : o.total;
+    };
+    if (tid == 96) {
+        uint32_t smid;
+        asm volatile("mov.u32 %0, %%smid;" : "=r"(smid));
+        if ((int)smid < o.reserve) limit = o.limit;
+        else if (o.reserve) atomicAdd(o.ready + o.total + 1, 1u);
+        slot[0] = take();
+        slot[1] = slot[0] < o.total ? take() : o.total;
+    }
+    __syncthreads();
     bool more = false, pending = false;
     Item x, nx;
-    if (i < o.total) {
-        x = item(o, i);
+    if (slot[0] < o.total) {
+        x = item(o, slot[0]);
         more = x.valid > 0;
     }
     if (more) {
@@ -200,19 +242,40 @@ operands_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             scan_gates<BWD>(vec(0), btot(0), rec_of(x), a.scale, ga, gb, lane);
         }
     }
-    bool next = more && i + step < o.total;
+    bool next = more && slot[1] < o.total;
     if (next) {
-        nx = item(o, i + step);
+        nx = item(o, slot[1]);
         next = nx.valid > 0;
         if (next && warp == 2) load_gates(nx);
     }
+    // thread 0: the block of the chunk before has been stored; say so
+    unsigned* done = nullptr;
+    auto publish = [&]() {
+        if (!done) return;
+        fence_proxy_async_global();
+        st_release_gpu(done, 1u);
+        done = nullptr;
+    };
     __syncthreads();
     for (int k = 0; more; ++k) {
         const GateVec gv = vec(k);
         const float* bt = btot(k);
         bool ok = true;
-        if (warp == 0) {
+        if (a.cu_s && x.valid < kChunk) {
+            // rows behind the sequence hold the next one's (or anything): make them zero, so
+            // that A and Att are zero there (a batch's rows past T were read as zeros)
             ok = wait_bar(&bars[0], k & 1, abort_flag);
+            for (int e = tid; e < 128 * 8 * (D / 64); e += kThreads) {
+                const int r = e & 127, c = e >> 7;
+                if ((r & 63) >= x.valid)
+                    *reinterpret_cast<uint4*>(sm + L::KQ + (c >> 3) * 16384 + sw128_off(r, c & 7)) =
+                        make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncthreads();
+        }
+        if (warp == 0) {
+            ok = wait_bar(&bars[0], k & 1, abort_flag) && ok;
             tc_fence_after_sync();
             __syncwarp();
             constexpr uint32_t id = idesc_bf16(128, 64, false, false);
@@ -223,58 +286,39 @@ operands_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 mma_bf16_elect(tmem, d, d, id, ks > 0);
             }
             mma_commit_elect(&bars[1]);
-            if (lane == 0) bulk_wait_group_read<0>();  // the last image has left
+            if (lane == 0) {  // the last image has left (overlapped: has been written)
+                if (done) {
+                    bulk_wait_group<0>();
+                    publish();
+                } else {
+                    bulk_wait_group_read<0>();
+                }
+            }
             __syncwarp();
         }
         ok = wait_bar(&bars[1], k & 1, abort_flag) && ok;
         if (!__syncthreads_and(ok)) break;
         tc_fence_after_sync();
+        int c2 = o.total;
         if (tid == 96) {
             pending = next;
-            if (next) load(nx);
+            if (next) {
+                load(nx);
+                c2 = take();  // waited for after the rows below
+            }
         }
         // ---- rows of A and Att, the diagonal 32 x 32 halves of T
         {
             const int r = tid & 63, R = r >> 4;
-            const bool att = warp >= 2, live = r < x.valid;
+            const bool att = warp >= 2, low = lane < 16;
             const uint32_t t0 = tmem + (static_cast<uint32_t>(warp * 32) << 16);
             const float ph = gv.at(kP, r), pl = gv.at(kPlo, r);
             // forward: column i carries beta_i; backward: row r of A carries beta_r
             const float lead = att ? a.scale : BWD ? gv.at(kBeta, r) : 1.f;
-            float fd[16];  // factors of this row's diagonal block
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const float4 p4 = gv.get4(kP, 4 * R + g), l4 = gv.get4(kPlo, 4 * R + g);
-                const float4 b4 = gv.get4(kBeta, 4 * R + g);
-                const float pv[4] = {p4.x, p4.y, p4.z, p4.w}, lv[4] = {l4.x, l4.y, l4.z, l4.w};
-                const float bv[4] = {b4.x, b4.y, b4.z, b4.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    fd[4 * g + e] = (BWD ? lead : lead * bv[e]) * __expf((ph - pv[e]) + (pl - lv[e]));
-            }
             const float ep = expf(ph);
             float off = lead * fmaf(ep, pl, ep);  // exp(p_r), then times the whole blocks between
-            const int last = r & 15;              // columns of the diagonal block that count
-            // row block R of lanes 16..31 is the warp's right-most column block
-#pragma unroll
-            for (int I = 3; I >= 0; --I) {
-                if (I > ((warp & 1) ? 3 : 1)) continue;  // right of every row of this warp
-                float g[16];
-                tmem_ld16(t0 + 16 * I, g);
-                tmem_wait_ld();
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float4 s4 = gv.get4(kSbeta, 4 * I + q);
-                    const float sv[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int j = 4 * q + e;
-                        const float f = I == R ? fd[j] : off * sv[e];
-                        const bool in = live && (I < R || (I == R && (att ? j <= last : j < last)));
-                        g[j] = in ? g[j] * f : 0.f;  // a select: what is masked may be NaN
-                    }
-                }
-                if (I < R) off *= bt[I];
+            const int last = (r & 15) + (att ? 1 : 0);  // columns of the diagonal block that count
+            auto put = [&](int I, const float (&g)[16]) {
                 if (att) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
@@ -293,7 +337,61 @@ operands_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                         *reinterpret_cast<float4*>(Am + r * LDA + 16 * I + j) =
                             make_float4(g[j], g[j + 1], g[j + 2], g[j + 3]);
                 }
+            };
+            // the two column blocks that hold the diagonal: a lane's own (its factors are the
+            // exponentials) and, for lanes 16..31, the one left of it
+            const int I0 = (warp & 1) * 2;
+            float fd[16];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float4 p4 = gv.get4(kP, 4 * R + q), l4 = gv.get4(kPlo, 4 * R + q);
+                const float4 b4 = gv.get4(kBeta, 4 * R + q);
+                const float pv[4] = {p4.x, p4.y, p4.z, p4.w}, lv[4] = {l4.x, l4.y, l4.z, l4.w};
+                const float bv[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    fd[4 * q + e] = (BWD ? lead : lead * bv[e]) * __expf((ph - pv[e]) + (pl - lv[e]));
             }
+#pragma unroll
+            for (int x2 = 1; x2 >= 0; --x2) {
+                const int I = I0 + x2;
+                float g[16];
+                tmem_ld16(t0 + 16 * I, g);
+                tmem_wait_ld();
+                const bool own = x2 == 0 ? low : !low;
+                const int upto = own ? last : x2 == 0 ? 16 : 0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float4 s4 = gv.get4(kSbeta, 4 * I + q);
+                    const float sv[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = 4 * q + e;
+                        const float f = own ? fd[j] : off * sv[e];
+                        g[j] = j < upto ? g[j] * f : 0.f;  // a select: what is masked may be NaN
+                    }
+                }
+                put(I, g);
+                if (x2 == 0 && !low) off *= bt[I];
+            }
+            // the blocks left of them: no mask, factors exp(p_r) . whole blocks . exp(s_i)
+            if (warp & 1)
+#pragma unroll
+                for (int I = 1; I >= 0; --I) {
+                    float g[16];
+                    tmem_ld16(t0 + 16 * I, g);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float4 s4 = gv.get4(kSbeta, 4 * I + q);
+                        g[4 * q] *= off * s4.x;
+                        g[4 * q + 1] *= off * s4.y;
+                        g[4 * q + 2] *= off * s4.z;
+                        g[4 * q + 3] *= off * s4.w;
+                    }
+                    put(I, g);
+                    off *= bt[I];
+                }
         }
         tc_fence_before_sync();
         if (warp < 2) {
@@ -321,40 +419,41 @@ operands_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             __syncwarp();
             // T_10 = -T_11 (A_10 T_00); the product in brackets above the diagonal
             float* lo = Am + (32 * warp) * LDA + 32 * warp;
-            const int rr = 2 * (lane >> 2), cc = 4 * (lane & 3);
             float acc[2][4];
-            tile_zero(acc);
-            tile_mm<false>(acc, lo + (16 + rr) * LDA, lo + cc, 0, 16);
-            tile_st(lo + rr * LDA + 16 + cc, acc);
+            block_zero(acc);
+            block_mm(acc, lo + 16 * LDA, lo, lane);
+            block_st(lo + 16, acc, 1.f, lane);
             __syncwarp();
-            tile_zero(acc);
-            tile_mm<true>(acc, lo + (16 + rr) * LDA + 16, lo + 16 + cc, 0, 16);
-            tile_st(lo + (16 + rr) * LDA + cc, acc);
+            block_zero(acc);
+            block_mm(acc, lo + 16 * LDA + 16, lo + 16, lane);
+            block_st(lo + 16 * LDA, acc, -1.f, lane);
         } else if (warp == 2 && next) {
             scan_gates<BWD>(vec(k + 1), btot(k + 1), rec_of(nx), a.scale, ga, gb, lane);
         }
-        const bool next2 = next && i + 2 * step < o.total;
+        if (tid == 96) slot[(k + 2) & 3] = c2;
+        __syncthreads();
         Item nx2 = nx;
-        bool n2 = false;
-        if (next2) {
-            nx2 = item(o, i + 2 * step);
+        bool n2 = next && slot[(k + 2) & 3] < o.total;
+        if (n2) {
+            nx2 = item(o, slot[(k + 2) & 3]);
             n2 = nx2.valid > 0;
             if (n2 && warp == 2) load_gates(nx2);
         }
-        __syncthreads();
         // ---- the two halves joined: M = A_10 T_00 (above the diagonal), T_10 = -T_11 M.
         // A warp takes 16 x 16 of the result; the 16 x 16 blocks above T_00's and T_11's own
         // diagonals (scratch, mathematically zero) are skipped.
         {
-            const int u = warp >> 1, v = warp & 1, rr = 2 * (lane >> 2), cc = 4 * (lane & 3);
+            const int u = warp >> 1, v = warp & 1;
             float acc[2][4];
-            tile_zero(acc);  // rows 16 v .., columns 16 u ..
-            tile_mm<false>(acc, Am + (32 + 16 * v + rr) * LDA, Am + 16 * u + cc, 16 * u, 32);
-            tile_st(Am + (16 * v + rr) * LDA + 32 + 16 * u + cc, acc);
+            block_zero(acc);  // rows 16 v .., columns 16 u ..
+            for (int k = u; k < 2; ++k)
+                block_mm(acc, Am + (32 + 16 * v) * LDA + 16 * k, Am + 16 * k * LDA + 16 * u, lane);
+            block_st(Am + 16 * v * LDA + 32 + 16 * u, acc, 1.f, lane);
             __syncthreads();
-            tile_zero(acc);  // rows 16 u .., columns 16 v ..
-            tile_mm<true>(acc, Am + (32 + 16 * u + rr) * LDA + 32, Am + 32 + 16 * v + cc, 0, 16 * (u + 1));
-            tile_st(Am + (32 + 16 * u + rr) * LDA + 16 * v + cc, acc);
+            block_zero(acc);  // rows 16 u .., columns 16 v ..
+            for (int k = 0; k <= u; ++k)
+                block_mm(acc, Am + (32 + 16 * u) * LDA + 32 + 16 * k, Am + 16 * k * LDA + 32 + 16 * v, lane);
+            block_st(Am + (32 + 16 * u) * LDA + 16 * v, acc, -1.f, lane);
         }
         __syncthreads();
         // ---- T in two bf16 terms: 320 pieces of 8 columns on and below the diagonal blocks
@@ -379,8 +478,8 @@ operands_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         if (tid == 0) {
             bulk_store(o.blk + ((size_t)x.n * a.H + x.h) * kBlock, sm + L::IMG, L::IMG_BYTES);
             bulk_commit_group();
+            if (o.reserve) done = o.ready + (size_t)x.n * a.H + x.h;
         }
-        i += step;
         more = next;
         x = nx;
         next = n2;
@@ -391,7 +490,10 @@ operands_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         (void)mbar_wait(&bars[0], 0);
         (void)mbar_wait(&bars[0], 1);
     }
-    if (tid == 0) bulk_wait_group_all();
+    if (tid == 0) {
+        bulk_wait_group_all();
+        publish();
+    }
     tc_fence_before_sync();
     __syncthreads();
     if (tid == 0 && *abort_flag) atomicOr(a.status + 1, 1u);
@@ -402,7 +504,7 @@ operands_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 }
 
 template <int D, bool BWD>
-cudaError_t launch_typed(const Args& a, cudaStream_t s)
+cudaError_t launch_typed(const Args& a, cudaStream_t s, int reserve, int limit)
 {
     using L = Lay<D, BWD>;
     CUtensorMap mq, mk;
@@ -420,6 +522,9 @@ cudaError_t launch_typed(const Args& a, cudaStream_t s)
     o.a = a;
     o.blk = a.blk;
     o.chunk_order = a.chunk_order;
+    o.ready = a.ready;
+    o.reserve = reserve;
+    o.limit = limit;
     o.total = (int)(chunks(a) * a.H);  // < 2^31
     if (o.total == 0) return cudaSuccess;
     const int grid = o.total < L::CTAS * sms ? o.total : L::CTAS * sms;
@@ -460,10 +565,11 @@ bool make_states_map(CUtensorMap* map, const void* base, const Args& a, int box_
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaError_t launch_operands_tc(const Args& a, cudaStream_t s, bool bwd)
+cudaError_t launch_operands_tc(const Args& a, cudaStream_t s, bool bwd, int reserve, int limit)
 {
-    if (bwd) return launch_typed<128, true>(a, s);
-    return a.D == 64 ? launch_typed<64, false>(a, s) : launch_typed<128, false>(a, s);
+    if (bwd) return launch_typed<128, true>(a, s, reserve, limit);
+    return a.D == 64 ? launch_typed<64, false>(a, s, reserve, limit)
+                     : launch_typed<128, false>(a, s, reserve, limit);
 }
 
 }  // namespace gdr

@@ -450,6 +450,11 @@ mdn_status mdn_chunk_fwd_noalloc(const void *q, const void *k, const void *v,
  * given (no clamp); scale is finite.  All states are fp32 and are held in
  * fp32 for the whole sequence.  Support: d_k = d_v in {64, 128}, C = 64, fp32
  * or bf16.
+ *
+ * bf16 chunk calls work on 64 tokens of a sequence at a time (forward d 64 and
+ * 128, backward d 128): there a value that is not finite reaches every token of
+ * its 64, the earlier ones too, and all after them.  alpha_log below -1e4
+ * counts as -1e4 (alpha is 0 in fp32 from -104 on).
  */
 
 /*
@@ -586,7 +591,7 @@ mdn_status mdn_gdr_step(const void *q, const void *k, const void *v, mdn_dtype i
  *               aligned; NULL where that is 0 (L = 1 and up to 256 channels a
  *               group at any alignment).
  * Any sizes with C % G = 0 and N G < 2^30, C < 2^22; N <= 65535 unless L = 1 and
- * C / G <= 256.  Pointers need the alignment of their element type (16-byte
+ * C / G <= 256; G <= 524280 unless L = 1.  Pointers need the alignment of their element type (16-byte
  * aligned tensors with groups of whole 16-byte pieces take a vectorised path).
  * Outputs may not alias inputs.  Asynchronous on `stream`.
  * Errors: MDN_ERR_INVALID_ARG, MDN_ERR_UNSUPPORTED, MDN_ERR_CUDA.

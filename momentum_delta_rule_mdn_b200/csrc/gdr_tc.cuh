@@ -220,24 +220,5 @@ bool make_states_map(CUtensorMap* map, const void* base, const Args& a, int box_
 // as this one's programmatic dependent finds those SMs free early.
 cudaError_t launch_operands_tc(const Args& a, cudaStream_t s, bool bwd, int reserve, int limit);
 
-// A kernel as the programmatic dependent of the one before it on s: its CTAs may start
-// while that one still runs, and read a chunk's block only after its ready flag.
-template <typename... P>
-cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, int threads, size_t shm, cudaStream_t s,
-                             const P&... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = shm;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 }  // namespace gdr
 }  // namespace mdn

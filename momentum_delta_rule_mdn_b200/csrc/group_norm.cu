@@ -26,6 +26,7 @@
 #include <type_traits>
 
 #include "mdn_internal.cuh"
+#include "sm100.cuh"
 
 namespace mdn {
 namespace gn {
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, NV * VEC <= 8 ? 4 : 2) tokens_fwd_ke
 #pragma unroll
         for (int t = 0; t < TOK; ++t) {
             if (!live[t]) continue;
-            const float mean = s[t], rstd = 1.f / sqrtf(q[t] * inv + a.eps);
+            const float mean = s[t], rstd = rsqrtf(q[t] * inv + a.eps);
             if (lane == 0) {
                 const size_t item = (size_t)(n0 + t * step + blockIdx.x * per + ts) * a.G + g;
                 a.mean[item] = mean;
@@ -264,6 +265,7 @@ __global__ void __launch_bounds__(kThreads, NV * VEC <= 8 ? 4 : 2) tokens_fwd_ke
 template <typename T, int VEC, int NV, int ACT, bool GATE>
 __global__ void __launch_bounds__(kThreads) tokens_bwd_kernel(const Args a, int lanes, int gslots)
 {
+    sm100::pdl_launch_dependents();
     const int Cg = a.C / a.G, units = Cg / VEC;
     const int lane = threadIdx.x % lanes, slot = threadIdx.x / lanes;
     const int per = kThreads / lanes / gslots;  // token slots of the block
@@ -383,14 +385,18 @@ __global__ void __launch_bounds__(kThreads) tokens_bwd_kernel(const Args a, int 
 }
 
 // The tokens form for groups of exactly LANES vectors (a power of two: head sizes).
-// The same mapping with nothing left to test per element; 8 of a token's 14 values a
-// thread are otherwise spent on it (issue-bound: 94 us instead of the figure below on
-// 32768 x 2048 gated bf16).
+// The same mapping with nothing left to test per element: 32768 x 2048 gated bf16 (403 MB)
+// take 71 us forward instead of 94, 5.7 TB/s; ungated 62 us (issue- and special-function-
+// bound: an exponential and a reciprocal per value).  The grid is what runs at once.
+// Backward keeps two tokens in flight per thread, as its registers admit two blocks per
+// SM only: 8192 x 1024 gated bf16 26.5 us instead of 28.5 with one.
 template <typename T, int LANES, int ACT, bool GATE, bool BWD>
 __global__ void __launch_bounds__(kThreads, BWD ? 2 : 4) tokens_exact_kernel(const Args a, int gslots)
 {
     constexpr int V = 16 / (int)sizeof(T), Cg = LANES * V;
     constexpr float inv = 1.f / Cg;
+    if (BWD) sm100::pdl_launch_dependents();
+    constexpr int AHEAD = BWD ? 2 : 1;  // tokens in flight per thread
     const int lane = threadIdx.x % LANES, slot = threadIdx.x / LANES;
     const int per = kThreads / LANES / gslots;
     const int g = blockIdx.y * gslots + slot % gslots, ts = slot / gslots;
@@ -404,32 +410,36 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 4) tokens_exact_kernel(con
         dw[e] = db[e] = 0.f;
     }
     const int step = gridDim.x * per;
-    int n = blockIdx.x * per + ts;
+    long long n = (long long)blockIdx.x * per + ts;
     const size_t hop = (size_t)step * a.G;
     size_t item = (size_t)n * a.G + g;
-    uint4 xr, zr, dr;
-    float mr = 0.f, rr = 0.f;
-    xr = zr = dr = make_uint4(0, 0, 0, 0);
-    auto fetch = [&](int n_, size_t it) {
+    struct Raw {
+        uint4 x, z, d;
+        float mean, rstd;
+    } raw[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) raw[u] = Raw{};
+    auto fetch = [&](Raw& f, long long n_, size_t it) {
         if (!(glive && n_ < a.N)) return;
         const size_t at = it * Cg + lane * V;
-        xr = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + at);
-        if (GATE) zr = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.gate) + at);
+        f.x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + at);
+        if (GATE) f.z = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.gate) + at);
         if (BWD) {
-            dr = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.dy) + at);
-            mr = a.mean[it];
-            rr = a.rstd[it];
+            f.d = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.dy) + at);
+            f.mean = a.mean[it];
+            f.rstd = a.rstd[it];
         }
     };
-    fetch(n, item);
-    for (int n0 = 0; n0 < a.N; n0 += step, n += step, item += hop) {  // uniform: shuffles below
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) fetch(raw[u], n + (long long)u * step, item + u * hop);
+    auto token = [&](Raw& f) {
         const bool live = glive && n < a.N;
         float v[V], z[V], d[V];
-        widen<T, V>(xr, v);
-        if (GATE) widen<T, V>(zr, z);
-        if (BWD) widen<T, V>(dr, d);
-        float mean = mr, rstd = rr;
-        fetch(n + step, item + hop);
+        widen<T, V>(f.x, v);
+        if (GATE) widen<T, V>(f.z, z);
+        if (BWD) widen<T, V>(f.d, d);
+        float mean = f.mean, rstd = f.rstd;
+        fetch(f, n + (long long)AHEAD * step, item + AHEAD * hop);
         const size_t at = item * Cg + lane * V;
         if (!BWD) {
             float s = 0.f, q = 0.f;
@@ -442,8 +452,8 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 4) tokens_exact_kernel(con
             for (int e = 0; e < V; ++e) q = fmaf(v[e] - mean, v[e] - mean, q);
 #pragma unroll
             for (int off = 1; off < LANES; off <<= 1) q += __shfl_xor_sync(0xffffffffu, q, off);
-            rstd = 1.f / sqrtf(q * inv + a.eps);
-            if (!live) continue;
+            rstd = rsqrtf(q * inv + a.eps);
+            if (!live) return;
             if (lane == 0) {
                 a.mean[item] = mean;
                 a.rstd[item] = rstd;
@@ -476,12 +486,16 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 4) tokens_exact_kernel(con
                 s1 += __shfl_xor_sync(0xffffffffu, s1, off);
                 s2 += __shfl_xor_sync(0xffffffffu, s2, off);
             }
-            if (!live) continue;
+            if (!live) return;
             if (GATE) stv<T, V>(static_cast<T*>(a.dgate) + at, z);
 #pragma unroll
             for (int e = 0; e < V; ++e) v[e] = rstd * (d[e] - s1 * inv - v[e] * (s2 * inv));
             stv<T, V>(static_cast<T*>(a.dx) + at, v);
         }
+    };
+    for (long long n0 = 0; n0 < a.N;) {  // uniform: shuffles in token()
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u, n0 += step, n += step, item += hop) token(raw[u]);
     }
     if (!BWD || !a.dweight) return;
     extern __shared__ float sh[];  // [2 V][kThreads]
@@ -537,6 +551,7 @@ __device__ __forceinline__ void join(float& k, float& mean, float& m2, float k2,
 template <typename T, bool BWD, int ACT, bool GATE>
 __global__ void __launch_bounds__(kThreads) rows_part_kernel(const Args a)
 {
+    sm100::pdl_launch_dependents();
     const int Cg = a.C / a.G, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int g = blockIdx.z * (kThreads / 32) + warp, n = blockIdx.y;
     if (g >= a.G) return;
@@ -628,20 +643,22 @@ __device__ __forceinline__ void join_parts(const Args& a, int n, int g0, int g1,
     for (int g = g0 + (int)threadIdx.x / 32; g < g1; g += kThreads / 32) {
         const float2* p = reinterpret_cast<const float2*>(a.part) + (size_t)n * a.blocks * a.G + g;
         if constexpr (!BWD) {
-            float k = 0.f, mean = 0.f, m2 = 0.f;
+            // sums about the first block's mean, then about the group's
+            const float e0 = p[0].x, all = (float)a.L * Cg;
+            auto count = [&](int b) { return (float)max(0, min(a.L, (b + 1) * per) - min(a.L, b * per)) * Cg; };
+            float s = 0.f, m2 = 0.f;
             for (int b = lane; b < a.blocks; b += 32) {
-                const int l0 = min(a.L, b * per), l1 = min(a.L, l0 + per);
+                const float k = count(b);
+                if (k > 0.f) s = fmaf(k, p[(size_t)b * a.G].x - e0, s);
+            }
+            const float mean = e0 + sum_lanes(s, 32) / all;
+            for (int b = lane; b < a.blocks; b += 32) {
                 const float2 v = p[(size_t)b * a.G];
-                if (l1 > l0) join(k, mean, m2, (float)(l1 - l0) * Cg, v.x, v.y);
+                const float k = count(b), d = v.x - mean;
+                if (k > 0.f) m2 += fmaf(k * d, d, v.y);
             }
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const float k2 = __shfl_xor_sync(0xffffffffu, k, off);
-                const float e2 = __shfl_xor_sync(0xffffffffu, mean, off);
-                const float q2 = __shfl_xor_sync(0xffffffffu, m2, off);
-                join(k, mean, m2, k2, e2, q2);
-            }
-            const float rstd = 1.f / sqrtf(m2 / ((float)a.L * Cg) + a.eps);
+            m2 = sum_lanes(m2, 32);
+            const float rstd = rsqrtf(m2 / all + a.eps);
             if (lane == 0) {
                 st[g - g0] = make_float2(mean, rstd);
                 if (blockIdx.x == 0) {
@@ -665,6 +682,9 @@ __device__ __forceinline__ void join_parts(const Args& a, int n, int g0, int g1,
     __syncthreads();
 }
 
+// The second pass.  Its rows do not depend on the first, so the first batch of them is
+// in flight while the statistics are joined, and each further one while its forerunner
+// is worked on.
 template <typename T, int ACT, bool GATE>
 __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(const Args a)
 {
@@ -672,24 +692,37 @@ __global__ void __launch_bounds__(kThreads) rows_fwd_kernel(const Args a)
     const int Cg = a.C / a.G, n = blockIdx.y, c = blockIdx.z * kThreads + threadIdx.x;
     const int g0 = blockIdx.z * kThreads / Cg;
     const int g1 = (min(a.C, (int)(blockIdx.z + 1) * kThreads) - 1) / Cg + 1;
-    join_parts<false>(a, n, g0, g1, st);
-    if (c >= a.C) return;
     const RowBlock rb = row_block(a);
-    const float2 ms = st[c / Cg - g0];
-    const float w = a.weight ? a.weight[c] : 1.f, b = a.weight ? a.bias[c] : 0.f;
+    const int l1 = c < a.C ? rb.l1 : 0;
+    const T* x = static_cast<const T*>(a.x);
     const T* gate = static_cast<const T*>(a.gate);
     size_t at = ((size_t)n * a.L + rb.l0) * a.C + c;
-    for (int l = rb.l0; l < rb.l1; l += kBatch, at += (size_t)kBatch * a.C) {
+    float xn[kBatch], zn[kBatch];
+    auto fetch = [&](int l, size_t from) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const bool in = l + u < l1;
+            xn[u] = in ? ld_elem(x + from + (size_t)u * a.C) : 0.f;
+            if (GATE) zn[u] = in ? ld_elem(gate + from + (size_t)u * a.C) : 0.f;
+        }
+    };
+    fetch(rb.l0, at);
+    const float w = a.weight && c < a.C ? a.weight[c] : 1.f, b = a.weight && c < a.C ? a.bias[c] : 0.f;
+    sm100::pdl_wait();  // for the partial statistics
+    join_parts<false>(a, n, g0, g1, st);
+    if (c >= a.C) return;
+    const float2 ms = st[c / Cg - g0];
+    for (int l = rb.l0; l < l1; l += kBatch, at += (size_t)kBatch * a.C) {
         float xv[kBatch], zv[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const bool in = l + u < rb.l1;
-            xv[u] = in ? ld_elem(static_cast<const T*>(a.x) + at + (size_t)u * a.C) : 0.f;
-            zv[u] = in && GATE ? ld_elem(gate + at + (size_t)u * a.C) : 0.f;
+            xv[u] = xn[u];
+            if (GATE) zv[u] = zn[u];
         }
+        fetch(l + kBatch, at + (size_t)kBatch * a.C);
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            if (l + u >= rb.l1) break;
+            if (l + u >= l1) break;
             const float nn = fmaf((xv[u] - ms.x) * ms.y, w, b);
             st_elem(static_cast<T*>(a.y) + at + (size_t)u * a.C,
                     GATE ? nn * act_of<ACT>(zv[u]) : act_of<ACT>(nn));
@@ -704,28 +737,48 @@ __global__ void __launch_bounds__(kThreads) rows_bwd_kernel(const Args a)
     const int Cg = a.C / a.G, n = blockIdx.y, c = blockIdx.z * kThreads + threadIdx.x;
     const int g0 = blockIdx.z * kThreads / Cg;
     const int g1 = (min(a.C, (int)(blockIdx.z + 1) * kThreads) - 1) / Cg + 1;
+    const RowBlock rb = row_block(a);
+    const int l1 = c < a.C ? rb.l1 : 0;
+    const T* x = static_cast<const T*>(a.x);
+    const T* dy = static_cast<const T*>(a.dy);
+    const T* gate = static_cast<const T*>(a.gate);
+    size_t at = ((size_t)n * a.L + rb.l0) * a.C + c;
+    float xn[kBatch], dn_[kBatch], zn[kBatch];
+    auto fetch = [&](int l, size_t from) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const bool in = l + u < l1;
+            xn[u] = in ? ld_elem(x + from + (size_t)u * a.C) : 0.f;
+            dn_[u] = in ? ld_elem(dy + from + (size_t)u * a.C) : 0.f;
+            if (GATE) zn[u] = in ? ld_elem(gate + from + (size_t)u * a.C) : 0.f;
+        }
+    };
+    sm100::pdl_launch_dependents();
+    fetch(rb.l0, at);
+    const int g = c / Cg;
+    float w = 1.f, b = 0.f, mean = 0.f, rstd = 0.f;
+    if (c < a.C) {
+        if (a.weight) w = a.weight[c], b = a.bias[c];
+        mean = a.mean[(size_t)n * a.G + g];
+        rstd = a.rstd[(size_t)n * a.G + g];
+    }
+    sm100::pdl_wait();  // for the partial sums
     join_parts<true>(a, n, g0, g1, st);
     if (c >= a.C) return;
-    const RowBlock rb = row_block(a);
-    const int g = c / Cg;
     const float2 m = st[g - g0];
-    const float mean = a.mean[(size_t)n * a.G + g], rstd = a.rstd[(size_t)n * a.G + g];
-    const float w = a.weight ? a.weight[c] : 1.f, b = a.weight ? a.bias[c] : 0.f;
-    const T* gate = static_cast<const T*>(a.gate);
     float dw = 0.f, db = 0.f;
-    size_t at = ((size_t)n * a.L + rb.l0) * a.C + c;
-    for (int l = rb.l0; l < rb.l1; l += kBatch, at += (size_t)kBatch * a.C) {
+    for (int l = rb.l0; l < l1; l += kBatch, at += (size_t)kBatch * a.C) {
         float xv[kBatch], dv[kBatch], zv[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const bool in = l + u < rb.l1;
-            xv[u] = in ? ld_elem(static_cast<const T*>(a.x) + at + (size_t)u * a.C) : 0.f;
-            dv[u] = in ? ld_elem(static_cast<const T*>(a.dy) + at + (size_t)u * a.C) : 0.f;
-            zv[u] = in && GATE ? ld_elem(gate + at + (size_t)u * a.C) : 0.f;
+            xv[u] = xn[u];
+            dv[u] = dn_[u];
+            if (GATE) zv[u] = zn[u];
         }
+        fetch(l + kBatch, at + (size_t)kBatch * a.C);
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            if (l + u >= rb.l1) break;
+            if (l + u >= l1) break;
             const size_t to = at + (size_t)u * a.C;
             const float h = (xv[u] - mean) * rstd, nn = fmaf(h, w, b);
             float f, df;
@@ -751,6 +804,7 @@ __global__ void __launch_bounds__(1024) wsum_kernel(const Args a)
     const long long c = (long long)blockIdx.x * 32 + threadIdx.x % 32;  // of [2, C]
     const int r0 = threadIdx.x / 32;
     float s = 0.f;
+    sm100::pdl_wait();  // for the partial rows
     if (c < 2LL * a.C)
         for (int r = r0; r < a.prows; r += 32 * 8) {
             float v[8];
@@ -800,9 +854,8 @@ Plan plan_of(int N, int L, int C, int G, bool f32, bool vec, bool bwd)
         p.gtiles = (G + p.gslots - 1) / p.gslots;
         const int per = slots / p.gslots;
         const int most = (N + per - 1) / per;
-        // forward: enough blocks to fill the SMs, several tokens each; backward fewer, since
-        // every block leaves a partial row of dw and db
-        p.blocks = std::max(1, std::min(most, std::max(1, (bwd ? want / 2 : want * 2) / p.gtiles)));
+        // as many blocks as run at once, several tokens each
+        p.blocks = std::max(1, std::min(most, std::max(1, 148 * (bwd ? 2 : 4) / p.gtiles)));
         p.prows = p.blocks;
     } else {
         // rows per block at least 16: the second pass rereads the partials of every block
@@ -854,8 +907,8 @@ cudaError_t fwd_typed(const Args& a, const Plan& p, cudaStream_t s)
     rows_part_kernel<T, false, ACT, GATE><<<g1, kThreads, 0, s>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    rows_fwd_kernel<T, ACT, GATE><<<dim3(p.blocks, a.N, (a.C + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(rows_fwd_kernel<T, ACT, GATE>, dim3(p.blocks, a.N, (a.C + kThreads - 1) / kThreads),
+                            kThreads, 0, s, a);
 }
 
 template <typename T, int ACT, bool GATE>
@@ -876,11 +929,12 @@ cudaError_t bwd_typed(const Args& a, const Plan& p, cudaStream_t s)
         const dim3 g1(p.blocks, a.N, (a.G + kThreads / 32 - 1) / (kThreads / 32));
         rows_part_kernel<T, true, ACT, GATE><<<g1, kThreads, 0, s>>>(a);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        rows_bwd_kernel<T, ACT, GATE><<<dim3(p.blocks, a.N, (a.C + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);
+        e = launch_dependent(rows_bwd_kernel<T, ACT, GATE>, dim3(p.blocks, a.N, (a.C + kThreads - 1) / kThreads),
+                             kThreads, 0, s, a);
+        if (e != cudaSuccess) return e;
     }
     if ((e = cudaGetLastError()) != cudaSuccess || !a.dweight) return e;
-    wsum_kernel<<<(2 * a.C + 31) / 32, 1024, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(wsum_kernel, dim3((2 * a.C + 31) / 32), 1024, 0, s, a);
 }
 
 template <typename T, bool BWD>
@@ -912,6 +966,7 @@ mdn_status check(int N, int L, int C, int G, mdn_dtype dt, int act)
     if (dt != MDN_F32 && dt != MDN_BF16) return MDN_ERR_UNSUPPORTED;
     // grid limits: rows and their groups per call, row blocks' second dimension
     if ((long long)N * G >= (1LL << 30) || C >= (1 << 22)) return MDN_ERR_UNSUPPORTED;
+    if (L > 1 && G > 8 * 65535) return MDN_ERR_UNSUPPORTED;  // 8 groups to a block of the rows form
     if (N > 65535) {  // only the tokens form takes more
         const Plan p = plan_of(N, L, C, G, dt == MDN_F32, true, true);
         const Plan q = plan_of(N, L, C, G, dt == MDN_F32, false, true);

@@ -391,4 +391,23 @@ cudaError_t launch_varlen_gather(const void* q, const void* k, const void* v, si
                                  int D, int NT, void* qp, void* kp, void* vp, float* alp,
                                  float* mlp, float* bep, float* etp, cudaStream_t s);
 
+// A kernel as the programmatic dependent of the one before it on s: its CTAs may start
+// once all of that one's have asked for it (or exited), while they still run.
+template <typename... P>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t shm, cudaStream_t s,
+                             const P&... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = shm;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace mdn

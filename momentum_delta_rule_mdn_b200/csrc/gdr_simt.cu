@@ -7,8 +7,9 @@
 // eighth float4 of rows; the 8 lanes that share a column reduce by shuffles.
 // One reduction per token is enough: with the state before the token,
 //     o_t = scale (alpha S^T q + beta (k.q) vtilde),
-// so S^T k and S^T q are summed together.  Bound by FMA issue: 3 d^2 per
-// token and head (49,152 at d = 128, 384 cycles of an SM).
+// so S^T k and S^T q are summed together; few chains share one among four tokens.
+// Many chains are bound by FMA issue: 3 d^2 per token and head (49,152 at d = 128,
+// 384 cycles of an SM); few by the latency of a token.
 #include "gdr_internal.cuh"
 
 namespace mdn {
@@ -28,6 +29,45 @@ __device__ __forceinline__ float lanes_sum(float x)
 {
 #pragma unroll
     for (int off = 1; off < RL; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    return x;
+}
+
+// Sums of 8 values over 8 lanes: lane rl returns the sum of value rl (7 shuffles; 24 if
+// every lane formed every sum).
+__device__ __forceinline__ float lanes_sum8(const float (&x)[8], int rl)
+{
+    float y[4], z[2];
+    const bool b4 = rl & 4, b2 = rl & 2, b1 = rl & 1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        y[i] = (b4 ? x[i + 4] : x[i]) + __shfl_xor_sync(0xffffffffu, b4 ? x[i] : x[i + 4], 4);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        z[i] = (b2 ? y[i + 2] : y[i]) + __shfl_xor_sync(0xffffffffu, b2 ? y[i] : y[i + 2], 2);
+    return (b1 ? z[1] : z[0]) + __shfl_xor_sync(0xffffffffu, b1 ? z[0] : z[1], 1);
+}
+// The same of 4 values: lane rl returns value rl % 4 (4 shuffles).
+__device__ __forceinline__ float lanes_sum4(const float (&x)[4], int rl)
+{
+    const bool b2 = rl & 2, b1 = rl & 1;
+    float z[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        z[i] = (b2 ? x[i + 2] : x[i]) + __shfl_xor_sync(0xffffffffu, b2 ? x[i] : x[i + 2], 2);
+    const float s = (b1 ? z[1] : z[0]) + __shfl_xor_sync(0xffffffffu, b1 ? z[0] : z[1], 1);
+    return s + __shfl_xor_sync(0xffffffffu, s, 4);
+}
+// Lane i's value of s into x[i], in every lane of the 8.
+template <int N>
+__device__ __forceinline__ void spread(float (&x)[N], float s)
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = __shfl_sync(0xffffffffu, s, i, 8);
+}
+__device__ __forceinline__ float warp_sum(float x)
+{
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
     return x;
 }
 
@@ -144,12 +184,146 @@ __device__ __forceinline__ float pick(const float (&x)[CPT], int rl)
     return y;
 }
 
-// ---------------------------------------------------------------- forward
-// One CTA: NC columns of one chain, CPT of them per thread.
-template <typename T, int D, int NC, int CPT>
-__global__ void __launch_bounds__(NC / CPT * RL) fwd_kernel(const Args a)
+// ---------------------------------------------------------------- few chains
+// With few chains a token's latency is the time, and most of it is the reduction.  So
+// GT = 4 tokens share one: their products with the state before all four are summed
+// together, and the three updates between are scalars per column, from the dot products
+// of the four tokens with one another (16 per four tokens, the same for every column).
+constexpr int GT = 4;
+constexpr int kFew = 16;  // columns of a CTA (32: 0.19 us a token at d 64, 8: 0.18, 16: 0.17)
+
+// Dot products inside every group of GT staged tokens, 8 lanes each: m[group][j][i] is
+// x_j . y_i for i <= j (REV: or, forward, for i >= j) and x_j . x_i on the other side.
+// Forward x = k, y = q; reverse x = q, y = k, and the other side is y_j . y_i.
+template <typename T, int TB, int D, int NT_, bool REV>
+__device__ __forceinline__ void grams(float (*m)[GT][GT], const T* ks, const T* qs)
 {
-    constexpr int NTH = NC / CPT * RL, V = D / (4 * RL), R = 4 * V;
+    for (int e = threadIdx.x / 8; e < TB / GT * GT * GT; e += NT_ / 8) {
+        const int g = e / (GT * GT), j = e / GT % GT, i = e % GT;
+        const bool kq = REV ? i <= j : i >= j;
+        // forward: k_j . q_i, else k_j . k_i; reverse: q_j . k_i, else k_j . k_i
+        const T* x = (REV && kq ? qs : ks) + (g * GT + j) * D;
+        const T* y = (!REV && kq ? qs : ks) + (g * GT + i) * D;
+        float s = 0.f;
+#pragma unroll
+        for (int c = (threadIdx.x % 8) * 4; c < D; c += 32) s = dot4(get4(x + c), get4(y + c), s);
+        s = lanes_sum(s);
+        if (threadIdx.x % 8 == 0) m[g][j][i] = s;
+    }
+}
+
+// Forward: with S the state before the group, u_i = S^T k_i and w_i = S^T q_i; token j
+// turns every later u_i into alpha_j u_i + beta_j (k_j . k_i) vtilde_j, and w likewise.
+template <typename T, int D, int NC>
+__global__ void __launch_bounds__(NC * RL) fwd_few_kernel(const Args a)
+{
+    constexpr int NTH = NC * RL, V = D / (4 * RL), R = 4 * V;
+    extern __shared__ __align__(16) uint8_t shm[];
+    const Buffers<T, TB, 2 * D + NC> buf{reinterpret_cast<T*>(shm)};  // k, q, v
+    __shared__ __align__(16) float al[TB], be[TB], gram[TB / GT][GT][GT];
+    const Chain ch = chain_of(a, blockIdx.x / (D / NC));
+    const int col0 = (blockIdx.x % (D / NC)) * NC;
+    const int tid = threadIdx.x, rl = tid % RL, c0 = tid / RL;
+    const size_t sbase = (size_t)ch.state * D * D + col0 + c0;
+    Part<D, 1> st;
+    st.load(a.S0 ? a.S0 + sbase : nullptr, rl);
+    T* const dst0 = static_cast<T*>(rl < GT ? a.o : a.vt);
+    const size_t hop = (size_t)GT * a.H * D;
+    float ga = 0.f, gb = 0.f;  // gates of token tid of the block being fetched
+    auto fetch = [&](int t0, int k) {
+        const int n = min(TB, ch.len - t0);
+        const long long row = ch.row0 + t0;
+        if (n > 0) {
+            stage<T, TB, D, D, NTH>(buf.at(k, 0), static_cast<const T*>(a.k), row, a.Hk, ch.hk, 0, n);
+            stage<T, TB, D, D, NTH>(buf.at(k, D), static_cast<const T*>(a.q), row, a.Hk, ch.hk, 0, n);
+            stage<T, TB, NC, D, NTH>(buf.at(k, 2 * D), static_cast<const T*>(a.v), row, a.H, ch.h, col0, n);
+            const bool in = tid < n;  // behind the sequence: no decay, no update
+            ga = in ? a.alpha_log[(row + tid) * a.H + ch.h] : 0.f;
+            gb = in ? a.beta[(row + tid) * a.H + ch.h] : 0.f;
+        }
+        stage_commit();
+    };
+    fetch(0, 0);
+    for (int t0 = 0, k = 0; t0 < ch.len; t0 += TB, ++k) {
+        const int n = min(TB, ch.len - t0);
+        const T* ks = buf.at(k, 0);
+        const T* qs = buf.at(k, D);
+        const T* vs = buf.at(k, 2 * D);
+        __syncthreads();  // the other buffer, al, be, gram are free
+        if (tid < TB) {
+            al[tid] = expf(ga);
+            be[tid] = gb;
+        }
+        fetch(t0 + TB, k + 1);
+        stage_wait();
+        __syncthreads();
+        grams<T, TB, D, NTH, false>(gram, ks, qs);
+        __syncthreads();
+        // lane j stores o of token j of a group, lane GT + j vtilde
+        T* dst = dst0;
+        if (dst) dst += ((size_t)(ch.row0 + t0 + rl % GT) * a.H + ch.h) * D + col0 + c0;
+#pragma unroll 1
+        for (int t = 0; t < n; t += GT) {
+            float kr[GT][R], x[2 * GT], v[GT];
+#pragma unroll
+            for (int j = 0; j < GT; ++j) {
+                float qr[R];
+                get_rows<V>(kr[j], ks + (t + j) * D, rl);
+                get_rows<V>(qr, qs + (t + j) * D, rl);
+                v[j] = ld_elem(vs + (t + j) * NC + c0);
+                x[j] = x[GT + j] = 0.f;
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    x[j] = fmaf(st.s[i][0], kr[j][i], x[j]);
+                    x[GT + j] = fmaf(st.s[i][0], qr[i], x[GT + j]);
+                }
+            }
+            const float4 a4 = get4(al + t), b4 = get4(be + t);
+            const float av[GT] = {a4.x, a4.y, a4.z, a4.w}, bv[GT] = {b4.x, b4.y, b4.z, b4.w};
+            spread(x, lanes_sum8(x, rl));
+            float c[GT];
+#pragma unroll
+            for (int j = 0; j < GT; ++j) {
+                const float4 m4 = get4(gram[t / GT][j]);
+                const float m[GT] = {m4.x, m4.y, m4.z, m4.w};
+                const float y = fmaf(-av[j], x[j], v[j]);
+                c[j] = t + j < n ? bv[j] * y : 0.f;
+                x[j] = y;
+#pragma unroll
+                for (int i = j + 1; i < GT; ++i) x[i] = fmaf(av[j], x[i], c[j] * gram[t / GT][i][j]);
+#pragma unroll
+                for (int i = 0; i < GT; ++i)
+                    x[GT + i] = i < j ? x[GT + i] : fmaf(av[j], x[GT + i], c[j] * m[i]);
+            }
+            float after = 1.f;  // decay of the tokens behind j
+#pragma unroll
+            for (int j = GT - 1; j >= 0; --j) {
+                c[j] *= after;
+                after *= av[j];
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                float s = st.s[i][0] * after;
+#pragma unroll
+                for (int j = 0; j < GT; ++j) s = fmaf(kr[j][i], c[j], s);
+                st.s[i][0] = s;
+            }
+            float y = 0.f;
+#pragma unroll
+            for (int i = 0; i < GT; ++i) y = rl % GT == i ? (rl < GT ? a.scale * x[GT + i] : x[i]) : y;
+            if (dst && t + rl % GT < n) st_elem(dst, y);
+            if (dst) dst += hop;
+        }
+    }
+    st.store(a.S_T + sbase, rl);
+}
+
+// ---------------------------------------------------------------- forward
+// One CTA: the D columns of one chain, CPT of them per thread.
+template <typename T, int D>
+__global__ void __launch_bounds__(D / 4 * RL) fwd_kernel(const Args a)
+{
+    constexpr int NC = D, CPT = 4, NTH = NC / CPT * RL, V = D / (4 * RL), R = 4 * V;
     extern __shared__ __align__(16) uint8_t shm[];
     const Buffers<T, TB, 2 * D + NC> buf{reinterpret_cast<T*>(shm)};  // k, q, v
     __shared__ float al[TB], be[TB], kq[TB];
@@ -231,10 +405,10 @@ __global__ void __launch_bounds__(NC / CPT * RL) fwd_kernel(const Args a)
 // ---------------------------------------------------------------- backward
 // S entering each chunk, from the saved vtilde (no chain of products: the
 // update of a token reads nothing of the state but its scale).
-template <typename T, int D, int NC, int CPT>
-__global__ void __launch_bounds__(NC / CPT * RL) states_kernel(const Args a)
+template <typename T, int D>
+__global__ void __launch_bounds__(D / 4 * RL) states_kernel(const Args a)
 {
-    constexpr int NTH = NC / CPT * RL, V = D / (4 * RL), R = 4 * V;
+    constexpr int NC = D, CPT = 4, NTH = NC / CPT * RL, V = D / (4 * RL), R = 4 * V;
     extern __shared__ __align__(16) uint8_t shm[];
     const Buffers<T, TB, D + NC> buf{reinterpret_cast<T*>(shm)};  // k, vtilde
     __shared__ float al[TB], be[TB];
@@ -292,10 +466,10 @@ __global__ void __launch_bounds__(NC / CPT * RL) states_kernel(const Args a)
 // The reverse chain: dv, the adjoint of S leaving each chunk, dS0.  As in the
 // forward pass one reduction per token: with the adjoint G' from the later
 // tokens, dv = beta (G'^T k + scale (q.k) do).
-template <typename T, int D, int NC, int CPT>
-__global__ void __launch_bounds__(NC / CPT * RL) reverse_kernel(const Args a)
+template <typename T, int D>
+__global__ void __launch_bounds__(D / 4 * RL) reverse_kernel(const Args a)
 {
-    constexpr int NTH = NC / CPT * RL, V = D / (4 * RL), R = 4 * V;
+    constexpr int NC = D, CPT = 4, NTH = NC / CPT * RL, V = D / (4 * RL), R = 4 * V;
     extern __shared__ __align__(16) uint8_t shm[];
     const Buffers<T, TB, 2 * D + NC> buf{reinterpret_cast<T*>(shm)};  // k, q, do
     __shared__ float al[TB], be[TB], kq[TB];
@@ -372,6 +546,187 @@ __global__ void __launch_bounds__(NC / CPT * RL) reverse_kernel(const Args a)
     g.store(a.dS0 + sbase, rl);
 }
 
+// Few chains: the two kernels above side by side (neither reads the other's results),
+// GT tokens at a time, one column a thread.
+template <typename T, int D, int NC>
+__device__ __forceinline__ void states_few(const Args& a, int block, uint8_t* shm, float* al, float* be)
+{
+    constexpr int NTH = NC * RL, V = D / (4 * RL), R = 4 * V;
+    const Buffers<T, TB, D + NC> buf{reinterpret_cast<T*>(shm)};  // k, vtilde
+    const Chain ch = chain_of(a, block / (D / NC));
+    const int col0 = (block % (D / NC)) * NC;
+    const int tid = threadIdx.x, rl = tid % RL, c0 = tid / RL;
+    const size_t sbase = (size_t)ch.state * D * D + col0 + c0;
+    Part<D, 1> st;
+    st.load(a.S0 ? a.S0 + sbase : nullptr, rl);
+    float ga = 0.f, gb = 0.f;
+    auto fetch = [&](int t0, int k) {
+        const int n = min(TB, ch.len - t0);
+        const long long row = ch.row0 + t0;
+        if (n > 0) {
+            stage<T, TB, D, D, NTH>(buf.at(k, 0), static_cast<const T*>(a.k), row, a.Hk, ch.hk, 0, n);
+            stage<T, TB, NC, D, NTH>(buf.at(k, D), static_cast<const T*>(a.vt), row, a.H, ch.h, col0, n);
+            const bool in = tid < n;
+            ga = in ? a.alpha_log[(row + tid) * a.H + ch.h] : 0.f;
+            gb = in ? a.beta[(row + tid) * a.H + ch.h] : 0.f;
+        }
+        stage_commit();
+    };
+    fetch(0, 0);
+    for (int t0 = 0, k = 0; t0 < ch.len; t0 += TB, ++k) {
+        if (t0 % kChunk == 0)
+            st.store(a.SS + ((size_t)(ch.chunk0 + t0 / kChunk) * a.H + ch.h) * D * D + col0 + c0, rl);
+        const T* ks = buf.at(k, 0);
+        const T* vs = buf.at(k, D);
+        __syncthreads();
+        if (tid < TB) {
+            al[tid] = expf(ga);
+            be[tid] = gb;
+        }
+        fetch(t0 + TB, k + 1);
+        stage_wait();
+        __syncthreads();
+        // all TB tokens: those behind the sequence are zero rows without decay
+#pragma unroll 1
+        for (int t = 0; t < TB; t += GT) {
+            const float4 a4 = get4(al + t), b4 = get4(be + t);
+            const float av[GT] = {a4.x, a4.y, a4.z, a4.w}, bv[GT] = {b4.x, b4.y, b4.z, b4.w};
+            float kr[GT][R], c[GT], after = 1.f;
+#pragma unroll
+            for (int j = GT - 1; j >= 0; --j) {
+                get_rows<V>(kr[j], ks + (t + j) * D, rl);
+                c[j] = bv[j] * ld_elem(vs + (t + j) * NC + c0) * after;
+                after *= av[j];
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                float s = st.s[i][0] * after;
+#pragma unroll
+                for (int j = 0; j < GT; ++j) s = fmaf(kr[j][i], c[j], s);
+                st.s[i][0] = s;
+            }
+        }
+    }
+}
+
+// With G' the adjoint behind the group, u_i = G'^T k_i; token j, from the last, gives
+// dv_j = beta_j (u_j + scale (q_j . k_j) do_j) and turns every earlier u_i into
+// alpha_j (u_i + scale (q_j . k_i) do_j - (k_j . k_i) dv_j).
+template <typename T, int D, int NC>
+__device__ __forceinline__ void reverse_few(const Args& a, int block, uint8_t* shm, float* al, float* be,
+                                            float (*gram)[GT][GT])
+{
+    constexpr int NTH = NC * RL, V = D / (4 * RL), R = 4 * V;
+    const Buffers<T, TB, 2 * D + NC> buf{reinterpret_cast<T*>(shm)};  // k, q, do
+    const Chain ch = chain_of(a, block / (D / NC));
+    const int col0 = (block % (D / NC)) * NC;
+    const int tid = threadIdx.x, rl = tid % RL, c0 = tid / RL;
+    const size_t sbase = (size_t)ch.state * D * D + col0 + c0;
+    Part<D, 1> g;
+    g.load(a.dS_T ? a.dS_T + sbase : nullptr, rl);
+    float ga = 0.f, gb = 0.f;
+    auto fetch = [&](int t0, int k) {
+        if (t0 >= 0) {
+            const int n = min(TB, ch.len - t0);
+            const long long row = ch.row0 + t0;
+            stage<T, TB, D, D, NTH>(buf.at(k, 0), static_cast<const T*>(a.k), row, a.Hk, ch.hk, 0, n);
+            stage<T, TB, D, D, NTH>(buf.at(k, D), static_cast<const T*>(a.q), row, a.Hk, ch.hk, 0, n);
+            stage<T, TB, NC, D, NTH>(buf.at(k, 2 * D), static_cast<const T*>(a.d_o), row, a.H, ch.h, col0, n);
+            const bool in = tid < n;
+            ga = in ? a.alpha_log[(row + tid) * a.H + ch.h] : 0.f;
+            gb = in ? a.beta[(row + tid) * a.H + ch.h] : 0.f;
+        }
+        stage_commit();
+    };
+    const int top = ch.len > 0 ? (ch.len - 1) / TB * TB : -TB;
+    fetch(top, 0);
+    for (int t0 = top, k = 0; t0 >= 0; t0 -= TB, ++k) {
+        const int n = min(TB, ch.len - t0);
+        if (t0 + n == ch.len || (t0 + TB) % kChunk == 0)
+            g.store(a.GG + ((size_t)(ch.chunk0 + t0 / kChunk) * a.H + ch.h) * D * D + col0 + c0, rl);
+        const T* ks = buf.at(k, 0);
+        const T* qs = buf.at(k, D);
+        const T* os = buf.at(k, 2 * D);
+        __syncthreads();
+        if (tid < TB) {
+            al[tid] = expf(ga);
+            be[tid] = gb;
+        }
+        fetch(t0 - TB, k + 1);
+        stage_wait();
+        __syncthreads();
+        grams<T, TB, D, NTH, true>(gram, ks, qs);
+        __syncthreads();
+        const size_t out0 = ((size_t)(ch.row0 + t0) * a.H + ch.h) * D + col0 + c0;
+#pragma unroll 1
+        for (int t = (n - 1) / GT * GT; t >= 0; t -= GT) {
+            float kr[GT][R], u[GT], h[GT], dv[GT];
+#pragma unroll
+            for (int j = 0; j < GT; ++j) {
+                get_rows<V>(kr[j], ks + (t + j) * D, rl);
+                h[j] = a.scale * ld_elem(os + (t + j) * NC + c0);
+                u[j] = 0.f;
+#pragma unroll
+                for (int i = 0; i < R; ++i) u[j] = fmaf(g.s[i][0], kr[j][i], u[j]);
+            }
+            const float4 a4 = get4(al + t), b4 = get4(be + t);
+            const float av[GT] = {a4.x, a4.y, a4.z, a4.w}, bv[GT] = {b4.x, b4.y, b4.z, b4.w};
+            spread(u, lanes_sum4(u, rl));
+#pragma unroll
+            for (int j = GT - 1; j >= 0; --j) {
+                const float4 m4 = get4(gram[t / GT][j]);
+                const float m[GT] = {m4.x, m4.y, m4.z, m4.w};
+                dv[j] = t + j < n ? bv[j] * fmaf(h[j], m[j], u[j]) : 0.f;
+#pragma unroll
+                for (int i = 0; i < j; ++i)
+                    u[i] = av[j] * fmaf(-dv[j], gram[t / GT][i][j], fmaf(h[j], m[i], u[i]));
+            }
+            {
+                const int j = rl % GT;
+                float y = 0.f;
+#pragma unroll
+                for (int i = 0; i < GT; ++i) y = j == i ? dv[i] : y;
+                if (rl < GT && t + j < n) {
+                    const size_t at = out0 + (size_t)(t + j) * a.H * D;
+                    a.dvf[at] = y;
+                    st_elem(static_cast<T*>(a.dv) + at, y);
+                }
+            }
+            float decay = 1.f;  // of the tokens up to j
+#pragma unroll
+            for (int j = 0; j < GT; ++j) {
+                decay *= av[j];
+                h[j] *= decay;
+                dv[j] *= decay;
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                g.s[i][0] *= decay;
+#pragma unroll
+                for (int j = 0; j < GT; ++j) g.s[i][0] = fmaf(-kr[j][i], dv[j], g.s[i][0]);
+            }
+#pragma unroll
+            for (int j = 0; j < GT; ++j) {
+                float qr[R];
+                get_rows<V>(qr, qs + (t + j) * D, rl);
+#pragma unroll
+                for (int i = 0; i < R; ++i) g.s[i][0] = fmaf(qr[i], h[j], g.s[i][0]);
+            }
+        }
+    }
+    g.store(a.dS0 + sbase, rl);
+}
+
+template <typename T, int D, int NC>
+__global__ void __launch_bounds__(NC * RL) back_few_kernel(const Args a)
+{
+    extern __shared__ __align__(16) uint8_t shm[];
+    __shared__ __align__(16) float al[TB], be[TB], gram[TB / GT][GT][GT];
+    const int half = gridDim.x / 2;
+    if ((int)blockIdx.x < half) reverse_few<T, D, NC>(a, blockIdx.x, shm, al, be, gram);
+    else states_few<T, D, NC>(a, blockIdx.x - half, shm, al, be);
+}
+
 // The token gradients of one chunk of one head, from the S entering it and
 // the adjoint of the S leaving it: rows of S and of G are independent here, so
 // a thread holds 4 rows and every eighth float4 of columns.  Forward over the
@@ -379,7 +734,7 @@ __global__ void __launch_bounds__(NC / CPT * RL) reverse_kernel(const Args a)
 // from   dalpha_log_t = dalpha_log_{t+1} + q.dq - beta dbeta - alpha k.(S dv),
 // started at the chunk's end with <G, S>, so that sums stay inside a chunk.
 template <typename T, int D>
-__global__ void __launch_bounds__(D * 2) token_grads_kernel(const Args a)
+__global__ void __launch_bounds__(D * 2, D == 64 ? 4 : 2) token_grads_kernel(const Args a)
 {
     constexpr int NTH = D * 2, V = D / (4 * RL), NW = NTH / 32, TB = kGradTokens;
     extern __shared__ __align__(16) uint8_t shm[];
@@ -448,11 +803,11 @@ __global__ void __launch_bounds__(D * 2) token_grads_kernel(const Args a)
         const T* c2 = buf.at(blk, D);
         const T* ks = buf.at(blk, 2 * D);
         const T* qs = buf.at(blk, 3 * D);
+#pragma unroll 2
         for (int t = 0; t < m; ++t) {
-            float po[4] = {0.f, 0.f, 0.f, 0.f}, pd[4] = {0.f, 0.f, 0.f, 0.f};
+            float p[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};  // S do, S dv of the 4 rows
             const float alpha = al[t], b = be[t];
-            const float4 k4 = get4(ks + t * D + row4), q4 = get4(qs + t * D + row4);
-            const float kr[4] = {k4.x, k4.y, k4.z, k4.w}, qr[4] = {q4.x, q4.y, q4.z, q4.w};
+            const float4 k4 = get4(ks + t * D + row4);
             const float bk[4] = {b * k4.x, b * k4.y, b * k4.z, b * k4.w};
 #pragma unroll
             for (int i = 0; i < V; ++i) {
@@ -462,33 +817,29 @@ __global__ void __launch_bounds__(D * 2) token_grads_kernel(const Args a)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float4 s4 = make_float4(s[r][4 * i], s[r][4 * i + 1], s[r][4 * i + 2], s[r][4 * i + 3]);
-                    po[r] = dot4(s4, o4, po[r]);
-                    pd[r] = dot4(s4, d4, pd[r]);
+                    p[r] = dot4(s4, o4, p[r]);
+                    p[4 + r] = dot4(s4, d4, p[4 + r]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         s[r][4 * i + e] = fmaf(alpha, s[r][4 * i + e], bk[r] * vv[e]);
                 }
             }
-            float share = 0.f;
-            float dq[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                dq[r] = a.scale * fmaf(alpha, lanes_sum(po[r]), bk[r] * dd[t]);
-                pd[r] = alpha * lanes_sum(pd[r]);
-                share += qr[r] * dq[r] - kr[r] * pd[r];
-            }
+            // lane r: dq of row r; lane 4 + r: alpha S dv of row r
+            const float x = alpha * lanes_sum8(p, rl);
+            const int row = row4 + rl % 4;
+            const float kv = ld_elem(ks + t * D + row), qv = ld_elem(qs + t * D + row);
             const size_t tok = (size_t)(cr.row0 + t0 + t);
+            float share;
             if (rl < 4) {
-                float y = dq[0], z = pd[0];
-                y = rl == 1 ? dq[1] : rl == 2 ? dq[2] : rl == 3 ? dq[3] : y;
-                z = rl == 1 ? pd[1] : rl == 2 ? pd[2] : rl == 3 ? pd[3] : z;
-                dks[t0 + t][row4 + rl] = z;
-                if (a.dqp) a.dqp[(tok * a.H + h) * D + row4 + rl] = y;
-                else st_elem(static_cast<T*>(a.dq) + (tok * a.Hk + hk) * D + row4 + rl, y);
+                const float y = a.scale * fmaf(b * kv, dd[t], x);
+                share = qv * y;
+                if (a.dqp) a.dqp[(tok * a.H + h) * D + row] = y;
+                else st_elem(static_cast<T*>(a.dq) + (tok * a.Hk + hk) * D + row, y);
+            } else {
+                share = -kv * x;
+                dks[t0 + t][row] = x;
             }
-            // the 4 row groups of the warp
-            share += __shfl_xor_sync(0xffffffffu, share, 8);
-            share += __shfl_xor_sync(0xffffffffu, share, 16);
+            share = warp_sum(share);
             if (lane == 0) cc[t0 + t][warp] = share;
         }
     }
@@ -502,8 +853,7 @@ __global__ void __launch_bounds__(D * 2) token_grads_kernel(const Args a)
                 const float4 g4 = *reinterpret_cast<const float4*>(a.GG + sbase + r * D + i * (4 * RL) + rl * 4);
                 x = dot4(g4, make_float4(s[r][4 * i], s[r][4 * i + 1], s[r][4 * i + 2], s[r][4 * i + 3]), x);
             }
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+        x = warp_sum(x);
         if (lane == 0) ip[warp] = x;
     }
     load(a.GG);
@@ -515,6 +865,7 @@ __global__ void __launch_bounds__(D * 2) token_grads_kernel(const Args a)
         const T* c0 = buf.at(blk, D);
         const T* ks = buf.at(blk, 2 * D);
         const T* qs = buf.at(blk, 3 * D);
+#pragma unroll 2
         for (int t = m - 1; t >= 0; --t) {
             float p[4] = {0.f, 0.f, 0.f, 0.f};
             const float alpha = al[t], b = be[t];
@@ -536,22 +887,18 @@ __global__ void __launch_bounds__(D * 2) token_grads_kernel(const Args a)
                         g = alpha * fmaf(-kr[r], dv[e], fmaf(sq[r], od[e], g));
                     }
             }
-            float share = 0.f;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                p[r] = fmaf(sq[r], dd[t], lanes_sum(p[r]));
-                share = fmaf(kr[r], p[r], share);
-            }
+            const float x = lanes_sum4(p, rl);
+            const int row = row4 + rl % 4;
             const size_t tok = (size_t)(cr.row0 + t0 + t);
-            if (rl < 4) {
-                float z = p[0];
-                z = rl == 1 ? p[1] : rl == 2 ? p[2] : rl == 3 ? p[3] : z;
-                const float y = fmaf(b, z, -dks[t0 + t][row4 + rl]);
-                if (a.dkp) a.dkp[(tok * a.H + h) * D + row4 + rl] = y;
-                else st_elem(static_cast<T*>(a.dk) + (tok * a.Hk + hk) * D + row4 + rl, y);
+            float share = 0.f;
+            if (rl < 4) {  // G vtilde of row rl
+                const float z = fmaf(a.scale * ld_elem(qs + t * D + row), dd[t], x);
+                share = ld_elem(ks + t * D + row) * z;
+                const float y = fmaf(b, z, -dks[t0 + t][row]);
+                if (a.dkp) a.dkp[(tok * a.H + h) * D + row] = y;
+                else st_elem(static_cast<T*>(a.dk) + (tok * a.Hk + hk) * D + row, y);
             }
-            share += __shfl_xor_sync(0xffffffffu, share, 8);
-            share += __shfl_xor_sync(0xffffffffu, share, 16);
+            share = warp_sum(share);
             if (lane == 0) bb[t0 + t][warp] = share;
         }
     }
@@ -635,37 +982,40 @@ cudaError_t run(K kernel, long long blocks, int threads, size_t shm, cudaStream_
     return cudaGetLastError();
 }
 
-// Columns per CTA and thread.  Few chains: 32 columns a CTA and one a thread, so
-// that a token costs a warp few instructions (with one warp per scheduler each
-// takes five to six cycles, whatever it does: four columns a thread took 0.94 us a
-// token at d = 64, one 0.20 us); while those CTAs are at most two per SM.  More: the whole head a CTA and
-// four columns a thread, which reads each staged k and q once for four columns.
+// Few chains, as long as CTAs of 32 columns are at most two per SM: one column a thread
+// and four tokens a reduction, so that a token costs a warp few instructions and little
+// waiting.  At d 64 a token takes 0.17 us in the forward pass and 0.15 in the reverse
+// chain, the states beside it (0.20, 0.23 and 0.09 for the states with a reduction per
+// token and 32 columns a CTA); bound by a warp's own latency, 3.6 cycles an instruction
+// with one warp per scheduler.  More chains: the whole head a CTA and four columns a thread, which reads each
+// staged k and q once for four columns.
 template <typename T, int D>
 cudaError_t fwd_typed(const Args& a, cudaStream_t s)
 {
     const long long n = chains(a);
     ProfScope ps(kGdrFwdSimt, s);
     if (n * (D / 32) <= 2LL * sm_count())
-        return run(fwd_kernel<T, D, 32, 1>, n * (D / 32), 32 * RL, 2 * TB * (2 * D + 32) * sizeof(T), s, a);
-    return run(fwd_kernel<T, D, D, 4>, n, 2 * D, 2 * TB * 3 * D * sizeof(T), s, a);
+        return run(fwd_few_kernel<T, D, kFew>, n * (D / kFew), kFew * RL, 2 * TB * (2 * D + kFew) * sizeof(T), s, a);
+    return run(fwd_kernel<T, D>, n, 2 * D, 2 * TB * 3 * D * sizeof(T), s, a);
 }
 
 template <typename T, int D>
 cudaError_t bwd_typed(const Args& a, cudaStream_t s)
 {
     const long long n = chains(a);
-    const bool narrow = n * (D / 32) <= 2LL * sm_count();
     cudaError_t e;
-    {
-        ProfScope ps(kGdrBwdStates, s);
-        e = narrow ? run(states_kernel<T, D, 32, 1>, n * (D / 32), 32 * RL, 2 * TB * (D + 32) * sizeof(T), s, a)
-                   : run(states_kernel<T, D, D, 4>, n, 2 * D, 2 * TB * 2 * D * sizeof(T), s, a);
-        if (e != cudaSuccess) return e;
-    }
-    {
+    if (n * (D / 32) <= 2LL * sm_count()) {
         ProfScope ps(kGdrBwdChain, s);
-        e = narrow ? run(reverse_kernel<T, D, 32, 1>, n * (D / 32), 32 * RL, 2 * TB * (2 * D + 32) * sizeof(T), s, a)
-                   : run(reverse_kernel<T, D, D, 4>, n, 2 * D, 2 * TB * 3 * D * sizeof(T), s, a);
+        e = run(back_few_kernel<T, D, kFew>, 2 * n * (D / kFew), kFew * RL, 2 * TB * (2 * D + kFew) * sizeof(T), s, a);
+        if (e != cudaSuccess) return e;
+    } else {
+        {
+            ProfScope ps(kGdrBwdStates, s);
+            e = run(states_kernel<T, D>, n, 2 * D, 2 * TB * 2 * D * sizeof(T), s, a);
+            if (e != cudaSuccess) return e;
+        }
+        ProfScope ps(kGdrBwdChain, s);
+        e = run(reverse_kernel<T, D>, n, 2 * D, 2 * TB * 3 * D * sizeof(T), s, a);
         if (e != cudaSuccess) return e;
     }
     const long long blocks = chunks(a) * a.H;

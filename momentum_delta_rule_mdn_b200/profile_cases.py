@@ -11,6 +11,10 @@ CASE      chunk      mdn_chunk_fwd over the workload's batch (both chunk kernels
           gates      mdn_gate_params on the workload's pre-activations
           bwd        mdn_chunk_bwd over the batch, from the forward pass's vtilde and a
                      seeded cotangent of o (every backward kernel)
+          gdr        mdn_gdr_chunk_fwd over the batch (the gated delta rule: operands, chain)
+          gdr_bwd    mdn_gdr_chunk_bwd over the batch (every backward kernel)
+          gdr_step   one mdn_gdr_step token for every head of the decode workload
+          norm       mdn_group_norm_fwd and _bwd, gated, over the batch's tokens and heads
 WORKLOAD  index or name of a synthetic workload (default 2, the 1.3B-layer shape)
 REPS      calls (default 3)
 
@@ -24,7 +28,7 @@ import torch
 
 import mdn_inputs as mi
 
-from . import api
+from . import api, gdr, norm
 
 
 def _spec(w: str) -> mi.Spec:
@@ -42,13 +46,16 @@ def main(argv) -> None:
     reps = int(argv[2]) if len(argv) > 2 else 3
     torch.cuda.set_device(0)
     gates = ("alpha_log", "mu_log", "beta", "eta")
-    if case == "step":
+    if case in ("step", "gdr_step"):
         dec = mi.WORKLOADS[4]
         tok = mi.make_inputs(mi.replace(dec, T=1, seed=dec.seed + 11))
         t = {k: v[:, 0].contiguous() for k, v in mi.to_torch(tok, "cuda").items() if v is not None}
         S = torch.randn((dec.B, dec.H, dec.d, dec.d), device="cuda") * 0.01
         M = torch.randn_like(S) * 0.01
-        for _ in range(reps):
+        for _ in range(reps if case == "gdr_step" else 0):
+            gdr.gdr_step(t["q"], t["k"], t["v"], t["alpha_log"], t["beta"], None, S,
+                         want_vtilde=False)
+        for _ in range(reps if case == "step" else 0):
             api.step(t["q"], t["k"], t["v"], *(t[g] for g in gates), dec.q_corr, S, M,
                      want_vtilde=False)
     else:
@@ -59,8 +66,21 @@ def main(argv) -> None:
             o, vt, _, _ = api.chunk_fwd(dev["q"], dev["k"], dev["v"], *(dev[g] for g in gates),
                                         inp.d_corr)
             do = torch.randn(o.shape, generator=torch.Generator().manual_seed(3)).to(o)
+        if case == "gdr_bwd":
+            o, vt, _ = gdr.gdr_chunk_fwd(dev["q"], dev["k"], dev["v"], dev["alpha_log"], dev["beta"])
+            do = torch.randn(o.shape, generator=torch.Generator().manual_seed(3)).to(o)
+        if case == "norm":
+            x, z = (dev[n].reshape(spec.B * spec.T, 1, -1) for n in ("v", "q"))
+            w, b = torch.ones(x.shape[2], device="cuda"), torch.zeros(x.shape[2], device="cuda")
         for _ in range(reps):
-            if case == "bwd":
+            if case == "gdr":
+                gdr.gdr_chunk_fwd(dev["q"], dev["k"], dev["v"], dev["alpha_log"], dev["beta"])
+            elif case == "gdr_bwd":
+                gdr.gdr_chunk_bwd(dev["q"], dev["k"], dev["alpha_log"], dev["beta"], None, vt, do)
+            elif case == "norm":
+                _, mean, rstd = norm.group_norm_fwd(x, spec.H, w, b, z)
+                norm.group_norm_bwd(x, spec.H, mean, rstd, x, w, b, z)
+            elif case == "bwd":
                 api.chunk_bwd(dev["q"], dev["k"], dev["v"], *(dev[g] for g in gates), inp.d_corr,
                               vt, do)
             elif case == "chunk":
@@ -77,7 +97,7 @@ def main(argv) -> None:
             else:
                 raise SystemExit(f"unknown case {case!r}")
     torch.cuda.synchronize()
-    print(f"{case} on {spec.name if case != 'step' else mi.WORKLOADS[4].name}: {reps} call(s) ok")
+    print(f"{case} on {spec.name if not case.endswith('step') else mi.WORKLOADS[4].name}: {reps} call(s) ok")
 
 
 if __name__ == "__main__":

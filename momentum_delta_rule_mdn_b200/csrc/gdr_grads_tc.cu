@@ -23,7 +23,7 @@
 // [K; Q] K^T and the P products, the rows of M (twelve warps, a 32 x 16 block each) and the
 // scaling of dO, Vtilde and dv in place, the products, the stores.  A scheduler with one
 // warp issues every fifth cycle at best, so the phases' work is spread over 16 warps (on 8
-// warps the kernel took 113 us at the 400M layer's shape).
+// warps the kernel took 113 us for 32 heads of 2048 tokens, on 16 it takes 73).
 #include "gdr_tc.cuh"
 
 namespace mdn {

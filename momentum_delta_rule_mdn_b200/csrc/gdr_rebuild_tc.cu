@@ -11,6 +11,7 @@
 // states' tile and every TMEM result are double-buffered.  Bound by issue (the
 // epilogues) and, for the outputs, by L2: per chunk and head 64 KB of fp32 states
 // (for <G, S>), 32 KB of bf16 states (for the token gradients) and 32 KB of XS.
+// 32 heads of 2048 tokens: 46 us, 1.4 us a chunk.
 //
 // Warps: 0 MMA issue, 1 loads, 16 chain warps (the state, K S and Q S as in the forward
 // chain), 4 warps that form gV, 1 that stores the bf16 states (TMA from a tile of their

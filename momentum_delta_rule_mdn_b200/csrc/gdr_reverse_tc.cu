@@ -13,8 +13,9 @@
 // the chunk before, the Q^T product under that of E'; the 4 output warps form
 // Diag(Dq) dO and store dv.  While the chain warps wait for products they take what the
 // gate gradients need: aC <G, S> with the state entering the chunk, vtilde . E (dbeta),
-// XS . dv and gam_r (G^T k_r) . vtilde_r, summed over this CTA's columns; and they store G in bf16 for the token
-// gradients.  Bounds and hand-offs as in the forward chain.
+// XS . dv and gam_r (G^T k_r) . vtilde_r, summed over this CTA's columns; and they
+// store G in bf16 for the token gradients.  Bounds and hand-offs as in the forward chain; 32 heads of 2048 tokens:
+// 75 us, 2.3 us a chunk (the forward chain's 1.65, two products and the gates' rows more).
 #include "gdr_tc.cuh"
 
 namespace mdn {

@@ -78,6 +78,8 @@ typedef enum {
                                  else 128 (packed sequences: 32 up to four waves, else
                                  64).  At most one; every width computes the same
                                  result; the flags exist for tuning and testing. */
+#define MDN_ZERO_BEHIND  0x40 /* mdn_gdr_chunk_*_varlen only: zeros in the output rows
+                                 behind the last sequence */
 #define MDN_TEST_NO_INTRA 0x100 /* testing the failure path only: the tensor-core
                                  path does not launch its intra-chunk kernel, so the
                                  inter-chunk kernel's wait for each chunk's operands
@@ -500,7 +502,8 @@ mdn_status mdn_gdr_chunk_fwd(const void *q, const void *k, const void *v, mdn_dt
  *   cu_seqlens  DEVICE pointer to N+1 ints, read on the device only:
  *               cu_seqlens[0] = 0, non-decreasing, cu_seqlens[N] <= total_T.
  *               Rows of o and vtilde behind cu_seqlens[N] are left as they
- *               were, and those of the inputs are not read into any result.
+ *               were (with MDN_ZERO_BEHIND they are set to zero), and those of
+ *               the inputs are not read into any result.
  *               Sequences may be empty (their S_T is S0).
  *   S0, S_T     [N,H,d,d].
  *
@@ -540,8 +543,9 @@ mdn_status mdn_gdr_chunk_bwd(const void *q, const void *k, mdn_dtype in_dtype,
                              mdn_stream_t stream);
 
 /* Gradients of mdn_gdr_chunk_fwd_varlen; shapes and cu_seqlens as there (rows
- * of the outputs behind the last sequence are left as they were; with broken
- * offsets dS0 is dS_T and nothing else is written). */
+ * of the outputs behind the last sequence are left as they were or, with
+ * MDN_ZERO_BEHIND, zero; with broken offsets dS0 is dS_T, and all rows are
+ * behind). */
 mdn_status mdn_gdr_chunk_bwd_varlen(const void *q, const void *k, mdn_dtype in_dtype,
                                     const float *alpha_log, const float *beta, float scale,
                                     const int *cu_seqlens, int N, int total_T, const float *S0,

@@ -12,6 +12,7 @@ MDN_OK, MDN_ERR_INVALID_ARG, MDN_ERR_UNSUPPORTED, MDN_ERR_CUDA, MDN_ERR_NONFINIT
 MDN_F32, MDN_BF16 = 0, 1
 MDN_CHECK_FINITE = 0x1
 MDN_FORCE_SIMT = 0x2
+MDN_ZERO_BEHIND = 0x40
 MDN_SLICE32 = 0x4
 MDN_SLICE64 = 0x8
 MDN_SLICE128 = 0x10

@@ -134,6 +134,50 @@ mdn_status begin(gdr::Args& a, const Sizes& z, const Layout& w, char* ws, const 
     return MDN_OK;
 }
 
+// MDN_ZERO_BEHIND: zeros in the rows of packed outputs behind the last sequence.
+struct Rest {
+    static constexpr int kMost = 5;
+    void* p[kMost];
+    size_t row_bytes[kMost];  // multiples of 4
+    int n;
+};
+
+__global__ void __launch_bounds__(256) zero_behind_kernel(const Rest r, const int* cu_s, int B, int total)
+{
+    const size_t rows = (size_t)(total - cu_s[B]), step = (size_t)gridDim.x * 256;
+    const size_t tid = (size_t)blockIdx.x * 256 + threadIdx.x;
+    for (int i = 0; i < r.n; ++i) {
+        char* p = static_cast<char*>(r.p[i]) + (size_t)cu_s[B] * r.row_bytes[i];
+        const size_t bytes = rows * r.row_bytes[i];
+        if (r.row_bytes[i] % 16 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+            for (size_t e = tid; e < bytes / 16; e += step) reinterpret_cast<uint4*>(p)[e] = make_uint4(0, 0, 0, 0);
+        } else {
+            for (size_t e = tid; e < bytes / 4; e += step) reinterpret_cast<unsigned*>(p)[e] = 0u;
+        }
+    }
+}
+
+// cu_s: the checked offsets, or null (no sequences: every row is behind).
+mdn_status zero_behind(const Rest& r, const int* cu_s, const Sizes& z, cudaStream_t s)
+{
+    cudaError_t e = cudaSuccess;
+    if (z.T == 0) return MDN_OK;
+    for (int i = 0; i < r.n && !cu_s; ++i) {
+        if (!r.p[i]) return MDN_ERR_INVALID_ARG;
+        if (e == cudaSuccess) e = cudaMemsetAsync(r.p[i], 0, (size_t)z.T * r.row_bytes[i], s);
+    }
+    if (cu_s) {
+        zero_behind_kernel<<<148 * 2, 256, 0, s>>>(r, cu_s, z.B, z.T);
+        e = cudaGetLastError();
+    }
+    return e == cudaSuccess ? MDN_OK : cuda_fail(e);
+}
+
+bool bad_flags(const Sizes& z, int flags)
+{
+    return flags & ~(MDN_CHECK_FINITE | MDN_FORCE_SIMT | (z.packed ? MDN_ZERO_BEHIND : 0));
+}
+
 struct Out {
     const void* p;
     size_t n;
@@ -162,8 +206,12 @@ mdn_status fwd_impl(const Sizes& z, const void* q, const void* k, const void* v,
 {
     mdn_status st = check_sizes(z);
     if (st != MDN_OK) return st;
-    if (flags & ~(MDN_CHECK_FINITE | MDN_FORCE_SIMT)) return MDN_ERR_INVALID_ARG;
+    if (bad_flags(z, flags)) return MDN_ERR_INVALID_ARG;
     if (!std::isfinite(scale)) return MDN_ERR_INVALID_ARG;
+    const size_t row = (size_t)z.H * z.dk * (z.dt == MDN_BF16 ? 2 : 4);
+    const Rest rest = {{o, vtilde}, {row, row}, vtilde ? 2 : 1};
+    if (z.B == 0 && z.H > 0 && (flags & MDN_ZERO_BEHIND))
+        return zero_behind(rest, nullptr, z, reinterpret_cast<cudaStream_t>(stream));
     if (z.B == 0 || z.H == 0) return MDN_OK;
     if (z.packed && (!cu_seqlens || !aligned4(cu_seqlens))) return MDN_ERR_INVALID_ARG;
     if (!S_T || !aligned16(S_T) || !aligned16(S0)) return MDN_ERR_INVALID_ARG;
@@ -184,6 +232,7 @@ mdn_status fwd_impl(const Sizes& z, const void* q, const void* k, const void* v,
     a.o = o; a.vt = vtilde; a.S_T = S_T;
     if (w.blk) a.blk = reinterpret_cast<uint8_t*>(ws + w.blk);
     if ((st = begin(a, z, w, ws, cu_seqlens, s)) != MDN_OK) return st;
+    if ((flags & MDN_ZERO_BEHIND) && (st = zero_behind(rest, a.cu_s, z, s)) != MDN_OK) return st;
     // no tokens: S_T = S0, which the CUDA-core kernel's walk over nothing gives
     const cudaError_t e = z.tc() && z.rows() > 0 ? gdr::launch_fwd_tc(a, s) : gdr::launch_fwd_simt(a, z.dt, s);
     if (e != cudaSuccess) return cuda_fail(e);
@@ -204,8 +253,12 @@ mdn_status bwd_impl(const Sizes& z, const void* q, const void* k, const float* a
 {
     mdn_status st = check_sizes(z);
     if (st != MDN_OK) return st;
-    if (flags & ~(MDN_CHECK_FINITE | MDN_FORCE_SIMT)) return MDN_ERR_INVALID_ARG;
+    if (bad_flags(z, flags)) return MDN_ERR_INVALID_ARG;
     if (!std::isfinite(scale)) return MDN_ERR_INVALID_ARG;
+    const size_t el = z.dt == MDN_BF16 ? 2 : 4, krow = z.Hk * z.dk * el, gate = (size_t)z.H * 4;
+    const Rest rest = {{dq, dk_out, dv_out, dalpha_log, dbeta}, {krow, krow, z.H * z.dk * el, gate, gate}, 5};
+    if (z.B == 0 && z.H > 0 && (flags & MDN_ZERO_BEHIND))
+        return zero_behind(rest, nullptr, z, reinterpret_cast<cudaStream_t>(stream));
     if (z.B == 0 || z.H == 0) return MDN_OK;
     if (z.packed && (!cu_seqlens || !aligned4(cu_seqlens))) return MDN_ERR_INVALID_ARG;
     if (!dS0 || !aligned16(dS0) || !aligned16(dS_T) || !aligned16(S0)) return MDN_ERR_INVALID_ARG;
@@ -237,6 +290,7 @@ mdn_status bwd_impl(const Sizes& z, const void* q, const void* k, const float* a
     a.gb = reinterpret_cast<__nv_bfloat16*>(at(w.gb));
     a.dvl = reinterpret_cast<__nv_bfloat16*>(at(w.dvl));
     if ((st = begin(a, z, w, ws, cu_seqlens, s)) != MDN_OK) return st;
+    if ((flags & MDN_ZERO_BEHIND) && (st = zero_behind(rest, a.cu_s, z, s)) != MDN_OK) return st;
     // no tokens: dS0 = dS_T, which the CUDA-core chain's walk over nothing gives
     const bool tc = z.bwd_tc() && z.rows() > 0;
     cudaError_t e = tc ? gdr::launch_bwd_tc(a, s) : gdr::launch_bwd_simt(a, z.dt, s);

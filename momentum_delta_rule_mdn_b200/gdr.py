@@ -15,6 +15,7 @@ stream of the work and of the tensors allocated for it.
 from __future__ import annotations
 
 import contextlib
+import functools
 import math
 from typing import Optional
 
@@ -52,8 +53,8 @@ class _On:
 def _need(t, like, dtype, shape, name):
     if t is None:
         return
-    if (t.dtype != dtype or t.shape != shape or not t.is_contiguous()
-            or t.device != like.device):
+    if (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
+            or t.get_device() != like.get_device()):
         raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {like.device}, got "
                          f"{t.dtype} {tuple(t.shape)} contiguous={t.is_contiguous()} on {t.device}")
 
@@ -77,11 +78,14 @@ def _scale(scale, d) -> float:
 
 
 def _workspace(ws, need, like):
+    """(pointer, bytes, tensor) of a call's scratch."""
     if ws is None:
-        return torch.empty(max(need, 1), dtype=torch.uint8, device=like.device)
-    if ws.device != like.device or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        if need == 0:
+            return None, 0, None
+        ws = like.new_empty(need, dtype=torch.uint8)
+    elif ws.device != like.device or ws.dtype != torch.uint8 or not ws.is_contiguous():
         raise ValueError("workspace: expected a contiguous uint8 tensor on the tensors' device")
-    return ws
+    return ws.data_ptr(), ws.numel(), ws
 
 
 def _cu(cu_seqlens, like):
@@ -97,9 +101,14 @@ def gdr_chunk_workspace_size(B: int, T: int, Hk: int, H: int, d: int, C: int = 6
                              dtype: torch.dtype = torch.bfloat16, flags: int = 0, *,
                              packed: bool = False, backward: bool = False) -> int:
     """Scratch bytes of the chunk calls (packed: B sequences in T tokens); 0 if unsupported."""
+    return _chunk_bytes(B, T, Hk, H, d, C, dtype, int(flags), packed, backward)
+
+
+@functools.lru_cache(maxsize=1024)
+def _chunk_bytes(B, T, Hk, H, d, C, dtype, flags, packed, backward):
     code = _lib.MDN_BF16 if dtype == torch.bfloat16 else _lib.MDN_F32
     name = f"mdn_gdr_chunk_{'bwd' if backward else 'fwd'}{'_varlen' if packed else ''}_workspace_size"
-    return int(getattr(library(), name)(B, T, Hk, H, d, d, C, code, int(flags)))
+    return int(getattr(library(), name)(B, T, Hk, H, d, d, C, code, flags))
 
 
 def _fwd(q, k, v, alpha_log, beta, scale, cu_seqlens, S0, C, out, want_vtilde, workspace, flags,
@@ -113,33 +122,34 @@ def _fwd(q, k, v, alpha_log, beta, scale, cu_seqlens, S0, C, out, want_vtilde, w
     _need(q, q, q.dtype, q.shape, "q")
     _need(k, q, q.dtype, q.shape, "k")
     _need(v, q, q.dtype, rows + (H, d), "v")
-    for name, t in (("alpha_log", alpha_log), ("beta", beta)):
-        _need(t, q, torch.float32, rows + (H,), name)
+    _need(alpha_log, q, torch.float32, rows + (H,), "alpha_log")
+    _need(beta, q, torch.float32, rows + (H,), "beta")
     _need(S0, q, torch.float32, (N, H, d, d), "S0")
+    flags = int(flags)
     scale = _scale(scale, d)
     with _On(q.device, stream) as s:
         if out is None:
-            # a packed buffer's rows behind the last sequence are not written
-            new = torch.zeros_like if packed else torch.empty_like
-            out = (new(v), new(v) if want_vtilde else None,
-                   torch.empty((N, H, d, d), dtype=torch.float32, device=q.device))
-        o, vt, S_T = out
-        _need(o, q, q.dtype, v.shape, "o")
-        _need(vt, q, q.dtype, v.shape, "vtilde")
-        _need(S_T, q, torch.float32, (N, H, d, d), "S_T")
+            o, vt = torch.empty_like(v), torch.empty_like(v) if want_vtilde else None
+            S_T = q.new_empty((N, H, d, d), dtype=torch.float32)
+            flags |= _lib.MDN_ZERO_BEHIND if packed else 0
+        else:
+            o, vt, S_T = out
+            _need(o, q, q.dtype, v.shape, "o")
+            _need(vt, q, q.dtype, v.shape, "vtilde")
+            _need(S_T, q, torch.float32, (N, H, d, d), "S_T")
         T = rows[-1]
-        ws = _workspace(workspace, gdr_chunk_workspace_size(N, T, Hk, H, d, C, q.dtype, flags,
-                                                            packed=packed), q)
+        ws, ws_bytes, _hold = _workspace(
+            workspace, _chunk_bytes(N, T, Hk, H, d, C, q.dtype, flags, packed, False), q)
         lib = library()
         if packed:
             status = lib.mdn_gdr_chunk_fwd_varlen(
                 _ptr(q), _ptr(k), _ptr(v), code, _ptr(alpha_log), _ptr(beta), scale,
                 _ptr(cu_seqlens), N, T, _ptr(S0), Hk, H, d, d, C, _ptr(o), _ptr(vt), _ptr(S_T),
-                _ptr(ws), ws.numel(), int(flags), s)
+                ws, ws_bytes, flags, s)
         else:
             status = lib.mdn_gdr_chunk_fwd(
                 _ptr(q), _ptr(k), _ptr(v), code, _ptr(alpha_log), _ptr(beta), scale, _ptr(S0), N, T,
-                Hk, H, d, d, C, _ptr(o), _ptr(vt), _ptr(S_T), _ptr(ws), ws.numel(), int(flags), s)
+                Hk, H, d, d, C, _ptr(o), _ptr(vt), _ptr(S_T), ws, ws_bytes, flags, s)
     _check(status, "mdn_gdr_chunk_fwd" + ("_varlen" if packed else ""))
     return o, vt, S_T
 
@@ -182,34 +192,33 @@ def _bwd(q, k, alpha_log, beta, cu_seqlens, scale, vtilde, d_o, S0, dS_T, C, wor
     code = _dtype_code(q)
     _need(q, q, q.dtype, q.shape, "q")
     _need(k, q, q.dtype, q.shape, "k")
-    for name, t in (("vtilde", vtilde), ("d_o", d_o)):
-        _need(t, q, q.dtype, rows + (H, d), name)
-    for name, t in (("alpha_log", alpha_log), ("beta", beta)):
-        _need(t, q, torch.float32, rows + (H,), name)
-    for name, t in (("S0", S0), ("dS_T", dS_T)):
-        _need(t, q, torch.float32, (N, H, d, d), name)
+    _need(vtilde, q, q.dtype, rows + (H, d), "vtilde")
+    _need(d_o, q, q.dtype, rows + (H, d), "d_o")
+    _need(alpha_log, q, torch.float32, rows + (H,), "alpha_log")
+    _need(beta, q, torch.float32, rows + (H,), "beta")
+    _need(S0, q, torch.float32, (N, H, d, d), "S0")
+    _need(dS_T, q, torch.float32, (N, H, d, d), "dS_T")
+    flags = int(flags) | (_lib.MDN_ZERO_BEHIND if packed else 0)
     scale = _scale(scale, d)
     with _On(q.device, stream) as s:
-        new = torch.zeros_like if packed else torch.empty_like
-        g = dict(zip(_GRADS, (new(q), new(k), new(vtilde), new(alpha_log), new(beta),
-                              torch.empty((N, H, d, d), dtype=torch.float32, device=q.device))))
+        g = [*map(torch.empty_like, (q, k, vtilde, alpha_log, beta)),
+             q.new_empty((N, H, d, d), dtype=torch.float32)]
         T = rows[-1]
-        ws = _workspace(workspace, gdr_chunk_workspace_size(N, T, Hk, H, d, C, q.dtype, flags,
-                                                            packed=packed, backward=True), q)
-        outs = [_ptr(g[n]) for n in _GRADS]
+        ws, ws_bytes, _hold = _workspace(
+            workspace, _chunk_bytes(N, T, Hk, H, d, C, q.dtype, flags, packed, True), q)
+        outs = [t.data_ptr() for t in g]
         lib = library()
         if packed:
             status = lib.mdn_gdr_chunk_bwd_varlen(
                 _ptr(q), _ptr(k), code, _ptr(alpha_log), _ptr(beta), scale, _ptr(cu_seqlens), N, T,
-                _ptr(S0), _ptr(vtilde), _ptr(d_o), _ptr(dS_T), Hk, H, d, d, C, *outs, _ptr(ws),
-                ws.numel(), int(flags), s)
+                _ptr(S0), _ptr(vtilde), _ptr(d_o), _ptr(dS_T), Hk, H, d, d, C, *outs, ws, ws_bytes,
+                flags, s)
         else:
             status = lib.mdn_gdr_chunk_bwd(
                 _ptr(q), _ptr(k), code, _ptr(alpha_log), _ptr(beta), scale, _ptr(S0), _ptr(vtilde),
-                _ptr(d_o), _ptr(dS_T), N, T, Hk, H, d, d, C, *outs, _ptr(ws), ws.numel(),
-                int(flags), s)
+                _ptr(d_o), _ptr(dS_T), N, T, Hk, H, d, d, C, *outs, ws, ws_bytes, flags, s)
     _check(status, "mdn_gdr_chunk_bwd" + ("_varlen" if packed else ""))
-    return g
+    return dict(zip(_GRADS, g))
 
 
 def gdr_chunk_bwd(q, k, alpha_log, beta, scale: Optional[float], vtilde, d_o, S0=None, dS_T=None,
@@ -244,18 +253,19 @@ def gdr_step(q, k, v, alpha_log, beta, scale: Optional[float], S: torch.Tensor, 
     _need(q, q, q.dtype, (B, Hk, d), "q")
     _need(k, q, q.dtype, (B, Hk, d), "k")
     _need(v, q, q.dtype, (B, H, d), "v")
-    for name, t in (("alpha_log", alpha_log), ("beta", beta)):
-        _need(t, q, torch.float32, (B, H), name)
+    _need(alpha_log, q, torch.float32, (B, H), "alpha_log")
+    _need(beta, q, torch.float32, (B, H), "beta")
+    _need(S, q, torch.float32, (B, H, d, d), "S")
+    _need(S_out, q, torch.float32, (B, H, d, d), "S_out")
+    _need(o, q, q.dtype, (B, H, d), "o")
+    _need(vtilde, q, q.dtype, (B, H, d), "vtilde")
     S_out = S if S_out is None else S_out
-    for name, t in (("S", S), ("S_out", S_out)):
-        _need(t, q, torch.float32, (B, H, d, d), name)
     scale = _scale(scale, d)
     with _On(q.device, stream) as s:
-        o = torch.empty_like(v) if o is None else o
+        if o is None:
+            o = torch.empty_like(v)
         if vtilde is None and want_vtilde:
             vtilde = torch.empty_like(v)
-        _need(o, q, q.dtype, (B, H, d), "o")
-        _need(vtilde, q, q.dtype, (B, H, d), "vtilde")
         status = library().mdn_gdr_step(
             _ptr(q), _ptr(k), _ptr(v), code, _ptr(alpha_log), _ptr(beta), scale, _ptr(S),
             _ptr(S_out), B, Hk, H, d, d, _ptr(o), _ptr(vtilde), 0, s)

@@ -11,6 +11,7 @@ over the L x C/groups values of a group.  The output of a token mixer,
 """
 from __future__ import annotations
 
+import functools
 from typing import Optional
 
 import torch
@@ -43,7 +44,11 @@ def _common(x, groups, weight, bias, gate, act):
 def group_norm_workspace_size(N: int, L: int, C: int, groups: int,
                               dtype: torch.dtype = torch.bfloat16, backward: bool = False) -> int:
     """Scratch bytes of :func:`group_norm_fwd` or :func:`group_norm_bwd`."""
-    code = _lib.MDN_BF16 if dtype == torch.bfloat16 else _lib.MDN_F32
+    return _bytes(N, L, C, groups, _lib.MDN_BF16 if dtype == torch.bfloat16 else _lib.MDN_F32, backward)
+
+
+@functools.lru_cache(maxsize=1024)
+def _bytes(N, L, C, groups, code, backward):
     return int(library().mdn_group_norm_workspace_size(N, L, C, groups, code, int(backward)))
 
 
@@ -55,16 +60,17 @@ def group_norm_fwd(x, groups: int, weight=None, bias=None, gate=None, eps: float
     N, L, C, code = _common(x, groups, weight, bias, gate, act)
     with _On(x.device, stream) as s:
         if out is None:
-            st = lambda: torch.empty((N, groups), dtype=torch.float32, device=x.device)
-            out = (torch.empty_like(x), st(), st())
-        y, mean, rstd = out
-        _need(y, x, x.dtype, x.shape, "y")
-        _need(mean, x, torch.float32, (N, groups), "mean")
-        _need(rstd, x, torch.float32, (N, groups), "rstd")
-        ws = _workspace(workspace, group_norm_workspace_size(N, L, C, groups, x.dtype), x)
+            y, mean = torch.empty_like(x), x.new_empty((N, groups), dtype=torch.float32)
+            rstd = torch.empty_like(mean)
+        else:
+            y, mean, rstd = out
+            _need(y, x, x.dtype, x.shape, "y")
+            _need(mean, x, torch.float32, (N, groups), "mean")
+            _need(rstd, x, torch.float32, (N, groups), "rstd")
+        ws, ws_bytes, _hold = _workspace(workspace, _bytes(N, L, C, groups, code, False), x)
         status = library().mdn_group_norm_fwd(
             _ptr(x), _ptr(gate), code, _ptr(weight), _ptr(bias), N, L, C, groups, float(eps),
-            _ACT[act], _ptr(y), _ptr(mean), _ptr(rstd), _ptr(ws), ws.numel(), s)
+            _ACT[act], _ptr(y), _ptr(mean), _ptr(rstd), ws, ws_bytes, s)
     _check(status, "mdn_group_norm_fwd")
     return y, mean, rstd
 
@@ -84,10 +90,10 @@ def group_norm_bwd(x, groups: int, mean, rstd, dy, weight=None, bias=None, gate=
             g["dgate"] = torch.empty_like(x)
         if weight is not None:
             g["dweight"], g["dbias"] = torch.empty_like(weight), torch.empty_like(bias)
-        ws = _workspace(workspace, group_norm_workspace_size(N, L, C, groups, x.dtype, True), x)
+        ws, ws_bytes, _hold = _workspace(workspace, _bytes(N, L, C, groups, code, True), x)
         status = library().mdn_group_norm_bwd(
             _ptr(x), _ptr(gate), code, _ptr(weight), _ptr(bias), _ptr(mean), _ptr(rstd), _ptr(dy),
             N, L, C, groups, _ACT[act], _ptr(g["dx"]), _ptr(g.get("dgate")), _ptr(g.get("dweight")),
-            _ptr(g.get("dbias")), _ptr(ws), ws.numel(), s)
+            _ptr(g.get("dbias")), ws, ws_bytes, s)
     _check(status, "mdn_group_norm_bwd")
     return g

@@ -94,7 +94,12 @@ def test_fwd_refusals(lib, varlen):
         assert _fwd(lib, varlen, **kw) == E.MDN_ERR_UNSUPPORTED, kw
     assert _fwd(lib, varlen, B=0, q=None, cu=None) == E.MDN_OK
     assert _fwd(lib, varlen, H=0, Hk=0, q=None) == E.MDN_OK
+    zero = E.MDN_ZERO_BEHIND
+    assert _fwd(lib, varlen, flags=zero, q=None) == E.MDN_ERR_INVALID_ARG
+    assert _fwd(lib, varlen, flags=zero, H=0, Hk=0, q=None) == (E.MDN_OK if varlen else E.MDN_ERR_INVALID_ARG)
     if varlen:
+        assert _fwd(lib, True, flags=zero, B=0, o=None) == E.MDN_ERR_INVALID_ARG
+        assert _fwd(lib, True, flags=zero, B=0, T=0, o=None) == E.MDN_OK
         assert _fwd(lib, True, cu=None) == E.MDN_ERR_INVALID_ARG
         assert _fwd(lib, True, cu=FAKE + 2) == E.MDN_ERR_INVALID_ARG
 

@@ -130,6 +130,25 @@ def test_many_short_sequences(dtype, d):
             assert R.rel(got[k], r) <= tol[got[k].dtype], (s, k)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("off", [(0,), (0, 0), (0, 3, 10), (0, 3, 11)])
+@pytest.mark.parametrize("H,Hk", [(1, 1), (6, 3)])
+def test_new_outputs_are_zero_behind_the_last_sequence(H, Hk, off, dtype):
+    """Freshly allocated outputs, on memory that held something else; with no sequence at all
+    every row is behind."""
+    x = inputs((11,), H, Hk, 64, dtype, 15)
+    cu = torch.tensor(off, dtype=torch.int32, device="cuda")
+    full = [torch.full((11, H, 64), 7.0, device="cuda", dtype=dtype) for _ in range(8)]
+    full += [torch.full((11, H), 7.0, device="cuda") for _ in range(4)]
+    del full
+    o, vt, S = mdn.gdr_chunk_fwd_varlen(x["q"], x["k"], x["v"], x["al"], x["be"], cu)
+    g = mdn.gdr_chunk_bwd_varlen(x["q"], x["k"], x["al"], x["be"], cu, None, vt, x["do"])
+    assert S.shape == g["dS0"].shape == (len(off) - 1, H, 64, 64)
+    for t in (o, vt, *(g[n] for n in ("dq", "dk", "dv", "dalpha_log", "dbeta"))):
+        assert (t[off[-1]:] == 0).all()
+        assert torch.isfinite(t).all() and (off[-1] == 0 or t[1:off[-1]].ne(0).any())
+
+
 @pytest.mark.parametrize("flags", [0, E.MDN_FORCE_SIMT])
 @pytest.mark.parametrize("dtype,d", [(BF16, 128), (BF16, 64), (F32, 64)])
 def test_minus_infinity_resets(dtype, d, flags):

@@ -542,14 +542,14 @@ cudaError_t launch_chain(const Args& a, bool overlap, cudaStream_t s)
 // critical path), so they keep 32 columns up to four waves.
 //
 // The chain is launched as the operand kernel's programmatic dependent.  Its CTAs need
-// a whole SM, so the operand CTAs on as many SMs as there are chain CTAs stop after L
-// chunks each, and those on the other SMs (U of them) make the rest, which the work
-// order makes the chunks the chains need last.  With r chain steps per operand chunk
-// (11k cycles at three CTAs an SM), L minimises  L r + max(NT, rest / U r + 1).  Measured,
-// operands and chain: 16384 tokens of 16 heads 350 -> 308 us, packed sequences of 1 to
-// 24576 tokens 792 -> 683 us, 4 x 2048 tokens of 8 heads 84 -> 77 us.  More chain CTAs
-// than SMs: nothing is reserved and nothing overlaps (in 8 x 4096 tokens of 16 heads the
-// flags cost 4% and the chain gained nothing).
+// a whole SM, so the operand CTAs on as many SMs as the chain's CTAs leave over beside
+// whole waves stop after L chunks each, and those on the other SMs (U of them) make the
+// rest, which the work order makes the chunks the chains need last; the chain's first,
+// partial wave runs meanwhile.  With r chain steps per operand chunk (11k cycles at three
+// CTAs an SM), L minimises  L r + max(NT, rest / U r + 1).  Measured, operands and chain:
+// 16384 tokens of 16 heads 350 -> 308 us, packed sequences of 1 to 24576 tokens 792 -> 683,
+// 4 x 2048 tokens of 8 heads 84 -> 77, 8 x 4096 of 16 (256 CTAs) 416 -> 393.  Whole waves
+// only: nothing is reserved and nothing overlaps.
 cudaError_t launch_fwd_tc(const Args& a, cudaStream_t s)
 {
     int dev = 0, sms = 148;
@@ -567,16 +567,17 @@ cudaError_t launch_fwd_tc(const Args& a, cudaStream_t s)
         // packed: SMs from the start for the chains of the longest sequence
         const long long first = (long long)a.H * (a.D / ns), room = sms - sms / 4;
         reserve = (int)(first < ctas ? (first < room ? first : room) : (ctas < room ? ctas : room));
-    } else if (ctas < sms) {
+    } else if (ctas % sms) {
         const double r = ns == 16 ? 5.0 : ns == 32 ? 3.9 : 2.5;
-        const long long U = 3LL * (sms - ctas), round = 3LL * sms, total = chunks(a) * a.H;
+        const long long first = ctas % sms;
+        const long long U = 3LL * (sms - first), round = 3LL * sms, total = chunks(a) * a.H;
         double best = 0.0;
         for (int L = 1; (L - 1) * round < total; ++L) {
             const long long rest = total - L * round;
             const double t = L * r + (rest > 0 ? fmax((double)a.NT, (double)rest / U * r + 1.0) : (double)a.NT);
             if (L == 1 || t < best) {
                 best = t;
-                reserve = (int)ctas;
+                reserve = (int)first;
                 limit = L;
             }
         }

@@ -19,11 +19,12 @@
 // bf16 terms.  The gate gradients are fp32: their products P1, P2 and [K; Q] K^T have
 // exact bf16 factors, dv in two terms.  P1 = dO Vtilde^T, P2 = dv Vtilde^T.
 //
-// One CTA per SM (176 KB of operands), bound by the latency of its phases: loads,
-// [K; Q] K^T and the P products, the rows of M (twelve warps, a 32 x 16 block each) and the
-// scaling of dO, Vtilde and dv in place, the products, the stores.  A scheduler with one
-// warp issues every fifth cycle at best, so the phases' work is spread over 16 warps (on 8
-// warps the kernel took 113 us for 32 heads of 2048 tokens, on 16 it takes 73).
+// One CTA per SM (176 KB of operands), walking the chunks; bound by the latency of its
+// phases: [K; Q] K^T and the P products, the rows of M (twelve warps, a 32 x 16 block
+// each) and the scaling of dO, Vtilde and dv in place, the products, the stores; the next
+// chunk's loads run under the last.  A scheduler with one warp issues every fifth cycle at
+// best, so the phases' work is spread over 16 warps.  32 heads of 2048 tokens: 62 us (one
+// CTA a chunk took 73, on 8 warps 113).
 #include "gdr_tc.cuh"
 
 namespace mdn {
@@ -61,23 +62,33 @@ struct GradMaps {
 };
 
 __global__ void __launch_bounds__(kThreads, 1)
-grads_kernel(const __grid_constant__ GradMaps tm, const Args a)
+grads_kernel(const __grid_constant__ GradMaps tm, const Args a, const long long total)
 {
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sbase = smem_u32(sm);
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int quad = warp & 3;
-    const long long n = blockIdx.x / a.Hk;
-    const int hk = blockIdx.x % a.Hk, rep = a.H / a.Hk;
-    const ChunkRows cr = chunk_rows(a, n);
-    if (cr.valid <= 0) return;
+    const int rep = a.H / a.Hk;
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + BARS);  // [0] K, Q; [1] rows; [2] S, G; [3] P; [4] sums
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + MISC + 4);
-    const int tb = a.cu_s ? 0 : (int)(n / a.NT);
-    const int tt = a.cu_s ? (int)cr.row0 : (int)(n % a.NT) * kChunk;
     const int SL = D / a.ns;
+    struct Item {
+        long long n;
+        int hk, tb, tt;
+        ChunkRows cr;
+    };
+    auto item = [&](long long i) {  // valid <= 0 past the last chunk with tokens
+        Item x;
+        x.n = i / a.Hk;
+        x.hk = (int)(i - x.n * a.Hk);
+        x.cr.valid = 0;
+        if (i < total) x.cr = chunk_rows(a, x.n);
+        x.tb = a.cu_s ? 0 : (int)(x.n / a.NT);
+        x.tt = a.cu_s ? (int)x.cr.row0 : (int)(x.n % a.NT) * kChunk;
+        return x;
+    };
 
     if (tid == 0) {
         for (int k = 0; k < 5; ++k) mbar_init(&bars[k], 1);
@@ -96,36 +107,39 @@ grads_kernel(const __grid_constant__ GradMaps tm, const Args a)
     const uint32_t tmem = *tmem_slot;
     const uint32_t tq = tmem + (static_cast<uint32_t>(quad * 32) << 16);
 
-    auto load_rows = [&](int h) {
-        mbar_arrive_expect_tx(&bars[1], 4 * 16384);
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            tma_load_4d(sm + DV + p * 16384, &tm.dv, p * 64, h, tt, tb, &bars[1]);
-            tma_load_4d(sm + DV + p * 16384 + 8192, &tm.d_o, p * 64, h, tt, tb, &bars[1]);
-            tma_load_4d(sm + VT + p * 8192, &tm.vt, p * 64, h, tt, tb, &bars[1]);
-            tma_load_4d(sm + DL + p * 8192, &tm.dvl, p * 64, h, tt, tb, &bars[1]);
-        }
-    };
-    auto load_states = [&](int h) {
-        mbar_arrive_expect_tx(&bars[2], 65536);
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            tma_load_3d(sm + SB + p * 16384, &tm.s, p * 64, 0, (int)(n * a.H + h), &bars[2]);
-            tma_load_3d(sm + GB + p * 16384, &tm.g, p * 64, 0, (int)(n * a.H + h), &bars[2]);
-        }
-    };
-    int loads = 0;  // heads whose loads were issued (thread 0), to drain after an abort
-    if (tid == 0) {
+    // one thread; S comes apart from the rest, as the outputs use its tile
+    auto load_keys = [&](const Item& x) {
         mbar_arrive_expect_tx(&bars[0], 32768);
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-            tma_load_4d(sm + KQ + p * 16384, &tm.k, p * 64, hk, tt, tb, &bars[0]);
-            tma_load_4d(sm + KQ + p * 16384 + 8192, &tm.q, p * 64, hk, tt, tb, &bars[0]);
+            tma_load_4d(sm + KQ + p * 16384, &tm.k, p * 64, x.hk, x.tt, x.tb, &bars[0]);
+            tma_load_4d(sm + KQ + p * 16384 + 8192, &tm.q, p * 64, x.hk, x.tt, x.tb, &bars[0]);
         }
-        load_rows(hk * rep);
-        load_states(hk * rep);
-        loads = 1;
+    };
+    auto load_head = [&](const Item& x, int h) {
+        mbar_arrive_expect_tx(&bars[1], 4 * 16384);
+        mbar_arrive_expect_tx(&bars[2], 65536);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            tma_load_4d(sm + VT + p * 8192, &tm.vt, p * 64, h, x.tt, x.tb, &bars[1]);
+            tma_load_4d(sm + DL + p * 8192, &tm.dvl, p * 64, h, x.tt, x.tb, &bars[1]);
+            tma_load_4d(sm + DV + p * 16384, &tm.dv, p * 64, h, x.tt, x.tb, &bars[1]);
+            tma_load_4d(sm + DV + p * 16384 + 8192, &tm.d_o, p * 64, h, x.tt, x.tb, &bars[1]);
+            tma_load_3d(sm + GB + p * 16384, &tm.g, p * 64, 0, (int)(x.n * a.H + h), &bars[2]);
+        }
+    };
+    auto load_s = [&](const Item& x, int h) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+            tma_load_3d(sm + SB + p * 16384, &tm.s, p * 64, 0, (int)(x.n * a.H + h), &bars[2]);
+    };
+    Item cur = item(blockIdx.x);
+    if (tid == 0 && cur.cr.valid > 0) {
+        load_keys(cur);
+        load_head(cur, cur.hk * rep);
+        load_s(cur, cur.hk * rep);
     }
+    int keys_in = 1, heads_in = 1;  // loads issued (thread 0), to drain after an abort
     const GateVec gv{sm + VEC, 16};
     float* bt = reinterpret_cast<float*>(sm + BT);
     float* rec = reinterpret_cast<float*>(sm + REC);
@@ -133,7 +147,9 @@ grads_kernel(const __grid_constant__ GradMaps tm, const Args a)
     float* rows = cs;
     float* gs = reinterpret_cast<float*>(sm + GS);
     // gate vectors, record and the chains' sums of a head: warps 8 .. 14, under the loads
-    auto head_scalars = [&](int h) {
+    auto head_scalars = [&](const Item& x, int h) {
+        const ChunkRows& cr = x.cr;
+        const long long n = x.n;
         if (warp == 8) {
             float ga[2], gb[2];
 #pragma unroll
@@ -176,21 +192,29 @@ grads_kernel(const __grid_constant__ GradMaps tm, const Args a)
             if (lane == 0) gs[256] = end;
         }
     };
-    head_scalars(hk * rep);
-
-    bool ok = wait_bar(&bars[0], 0, abort_flag);
-    if (a.cu_s && cr.valid < kChunk) {
-        // K and Q rows behind the sequence meet zeros of M: make them zero
-        for (int e = tid; e < 128 * 16; e += kThreads) {
-            const int r = e >> 4, p = e & 15;
-            if ((r & 63) >= cr.valid)
-                *reinterpret_cast<uint4*>(sm + KQ + (p >> 3) * 16384 + sw128_off(r, p & 7)) = make_uint4(0, 0, 0, 0);
+    if (cur.cr.valid > 0) head_scalars(cur, cur.hk * rep);
+    bool ok = true;
+    int u = 0;  // heads processed: the phase of their barriers
+    for (int it = 0; cur.cr.valid > 0; ++it) {
+        const ChunkRows cr = cur.cr;
+        const long long n = cur.n;
+        const int hk = cur.hk;
+        const Item nx = item(blockIdx.x + (long long)(it + 1) * gridDim.x);
+        if (a.cu_s && cr.valid < kChunk) {
+            ok = wait_bar(&bars[0], it & 1, abort_flag);
+            // K and Q rows behind the sequence meet zeros of M: make them zero
+            for (int e = tid; e < 128 * 16; e += kThreads) {
+                const int r = e >> 4, p = e & 15;
+                if ((r & 63) >= cr.valid)
+                    *reinterpret_cast<uint4*>(sm + KQ + (p >> 3) * 16384 + sw128_off(r, p & 7)) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncthreads();
         }
-        fence_proxy_async_smem();
-    }
-    ok = __syncthreads_and(ok);
-    if (ok) {
         if (warp == 0) {  // [K; Q] K^T
+            ok = wait_bar(&bars[0], it & 1, abort_flag) && ok;
+            tc_fence_after_sync();
+            __syncwarp();
             constexpr uint32_t id = idesc_bf16(128, 64, false, false);
             const uint64_t d0 = smem_desc(sbase + KQ, 16, 1024, kSw128);
 #pragma unroll
@@ -199,11 +223,10 @@ grads_kernel(const __grid_constant__ GradMaps tm, const Args a)
                 mma_bf16_elect(tmem + TM_G, d, d, id, ks > 0);
             }
         }
-        for (int hh = 0; hh < rep; ++hh) {
+        for (int hh = 0; hh < rep; ++hh, ++u) {
             const int h = hk * rep + hh;
-            const size_t hcn = (size_t)n * a.H + h;
             if (warp == 0) {
-                ok = wait_bar(&bars[1], hh & 1, abort_flag);
+                ok = wait_bar(&bars[1], u & 1, abort_flag) && ok;
                 tc_fence_after_sync();
                 __syncwarp();
                 constexpr uint32_t id = idesc_bf16(128, 64, false, false);
@@ -220,7 +243,7 @@ grads_kernel(const __grid_constant__ GradMaps tm, const Args a)
                 }
                 mma_commit_elect(&bars[3]);
             }
-            ok = wait_bar(&bars[3], hh & 1, abort_flag) && ok;
+            ok = wait_bar(&bars[3], u & 1, abort_flag) && ok;
             if (!(ok = __syncthreads_and(ok))) break;
             tc_fence_after_sync();
             // ---- rows of -M2 (lanes 0..63) and M1, and the sums of Z: a warp takes 32 rows and one
@@ -308,7 +331,7 @@ grads_kernel(const __grid_constant__ GradMaps tm, const Args a)
             __syncthreads();
             tc_fence_after_sync();
             if (warp == 0) {
-                ok = wait_bar(&bars[2], hh & 1, abort_flag);
+                ok = wait_bar(&bars[2], u & 1, abort_flag);
                 __syncwarp();
                 constexpr uint32_t ids = idesc_bf16(64, 128, false, false);   // rows . state^T
                 constexpr uint32_t idm = idesc_bf16(64, 128, false, true);    // M . rows
@@ -381,19 +404,27 @@ grads_kernel(const __grid_constant__ GradMaps tm, const Args a)
                     }
                 }
             }
-            ok = wait_bar(&bars[4], hh & 1, abort_flag) && ok;
+            ok = wait_bar(&bars[4], u & 1, abort_flag) && ok;
             if (!(ok = __syncthreads_and(ok))) break;
             tc_fence_after_sync();
-            if (tid == 0 && hh + 1 < rep) {
-                load_rows(h + 1);
-                load_states(h + 1);
-                loads = hh + 2;
+            if (hh + 1 < rep) {
+                if (tid == 0) {
+                    load_head(cur, h + 1);
+                    load_s(cur, h + 1);
+                    ++heads_in;
+                }
+                head_scalars(cur, h + 1);
             }
-            if (hh + 1 < rep) head_scalars(h + 1);
         }
-    }
-    if (ok) {
-        // ---- dq, dk: bf16 through the rows' tile; a warp 64 columns of 16 rows of one of them
+        if (!ok) break;
+        // the next chunk's tiles are on their way while this one's dq and dk leave
+        if (tid == 0 && nx.cr.valid > 0) {
+            load_keys(nx);
+            load_head(nx, nx.hk * rep);
+            ++keys_in;
+            ++heads_in;
+        }
+        // ---- dq, dk: bf16 through the tile of S; a warp 64 columns of 16 rows of one of them
         const int r0 = quad * 16 + (lane >> 2), pc = (lane & 3) * 4, half = (warp >> 2) & 1, w = warp >> 3;
         float x[32];
         tmem_ld_16x256<8>(tq + (w ? TM_K : TM_Q) + 64 * half, x);
@@ -402,17 +433,17 @@ grads_kernel(const __grid_constant__ GradMaps tm, const Args a)
         for (int c = 0; c < 8; ++c)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-                *reinterpret_cast<uint32_t*>(sm + DV + w * 16384 + half * 8192 + sw128_off(r0 + 8 * e, c) + pc) =
+                *reinterpret_cast<uint32_t*>(sm + SB + w * 16384 + half * 8192 + sw128_off(r0 + 8 * e, c) + pc) =
                     pack_bf16(x[4 * c + 2 * e], x[4 * c + 2 * e + 1]);
         fence_proxy_async_smem();
         tc_fence_before_sync();
         __syncthreads();
         if (!a.cu_s || cr.valid == kChunk) {
-            if (tid == 0) {
+            if (tid == kThreads - 32) {  // a warp with nothing else to do until the next rows
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    tma_store_4d(&tm.dq, p * 64, hk, tt, tb, sm + DV + p * 8192);
-                    tma_store_4d(&tm.dk, p * 64, hk, tt, tb, sm + DV + 16384 + p * 8192);
+                    tma_store_4d(&tm.dq, p * 64, hk, cur.tt, cur.tb, sm + SB + p * 8192);
+                    tma_store_4d(&tm.dk, p * 64, hk, cur.tt, cur.tb, sm + SB + 16384 + p * 8192);
                 }
                 bulk_commit_group();
                 bulk_wait_group_read<0>();
@@ -423,14 +454,24 @@ grads_kernel(const __grid_constant__ GradMaps tm, const Args a)
                 if (r < cr.valid)
                     *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(w ? a.dk : a.dq) +
                                               ((size_t)(cr.row0 + r) * a.Hk + hk) * D + 8 * c) =
-                        *reinterpret_cast<const uint4*>(sm + DV + w * 16384 + (c >> 3) * 8192 + sw128_off(r, c & 7));
+                        *reinterpret_cast<const uint4*>(sm + SB + w * 16384 + (c >> 3) * 8192 + sw128_off(r, c & 7));
             }
         }
-    } else if (tid == 0) {
+        if (nx.cr.valid > 0) {
+            if (a.cu_s && cr.valid < kChunk) __syncthreads();  // the tile has been read
+            if (tid == kThreads - 32) {
+                fence_proxy_async_smem();
+                load_s(nx, nx.hk * rep);
+            }
+            head_scalars(nx, nx.hk * rep);
+        }
+        cur = nx;
+    }
+    if (!ok && tid == 0) {
         // after an abort: copies in flight land before shared memory is released
-        (void)mbar_wait(&bars[0], 0);
-        (void)mbar_wait(&bars[1], (loads - 1) & 1);
-        (void)mbar_wait(&bars[2], (loads - 1) & 1);
+        (void)mbar_wait(&bars[0], (keys_in - 1) & 1);
+        (void)mbar_wait(&bars[1], (heads_in - 1) & 1);
+        (void)mbar_wait(&bars[2], (heads_in - 1) & 1);
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -466,7 +507,11 @@ cudaError_t launch_bwd_tc(const Args& a, cudaStream_t s)
     const long long blocks = chunks(a) * a.Hk;
     if (blocks == 0) return cudaSuccess;
     ProfScope ps(kGdrBwdGrads, s);
-    grads_kernel<<<(unsigned)blocks, kThreads, BYTES, s>>>(m, a);
+    int dev = 0, sms = 148;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess ||
+        (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+        return e;
+    grads_kernel<<<(unsigned)(blocks < sms ? blocks : sms), kThreads, BYTES, s>>>(m, a, blocks);
     return cudaGetLastError();
 }
 

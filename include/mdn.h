@@ -484,8 +484,8 @@ size_t mdn_gdr_chunk_bwd_varlen_workspace_size(int N, int total_T, int Hk, int H
  *               Calls that may overlap need workspaces of their own.
  *   flags       MDN_CHECK_FINITE and/or MDN_FORCE_SIMT.
  *
- * Any T >= 0 (T = 0 copies S0 to S_T).  Pointers to q, k, v, o, vtilde and the
- * states are 16-byte aligned.  Asynchronous on `stream` (except with
+ * Any T >= 0 (T = 0 copies S0 to S_T).  Outputs may not alias inputs, S_T = S0
+ * apart.  Pointers to q, k, v, o, vtilde and the states are 16-byte aligned.  Asynchronous on `stream` (except with
  * MDN_CHECK_FINITE); can be captured in a CUDA graph.  The workspace's status
  * words can be read with mdn_chunk_fwd_status.  Errors as mdn_chunk_fwd.
  */
@@ -565,7 +565,7 @@ mdn_status mdn_gdr_chunk_bwd_varlen(const void *q, const void *k, mdn_dtype in_d
  *   o           [B,H,d] in_dtype; vtilde the same or NULL.
  *   flags       must be 0 (reserved).
  * S and S_out 16-byte aligned, every other pointer aligned to its element
- * type.  Each state element is read once and written once.
+ * type; o and vtilde may not alias inputs.  Each state element is read once and written once.
  * Errors: MDN_ERR_INVALID_ARG, MDN_ERR_UNSUPPORTED, MDN_ERR_CUDA.
  */
 mdn_status mdn_gdr_step(const void *q, const void *k, const void *v, mdn_dtype in_dtype,
@@ -595,7 +595,8 @@ mdn_status mdn_gdr_step(const void *q, const void *k, const void *v, mdn_dtype i
  *               aligned; NULL where that is 0 (L = 1 and up to 256 channels a
  *               group at any alignment).
  * Any sizes with C % G = 0 and N G < 2^30, C < 2^22; N <= 65535 unless L = 1 and
- * C / G <= 256; G <= 524280 unless L = 1.  Pointers need the alignment of their element type (16-byte
+ * C / G <= 256; G <= 524280 unless L = 1;
+ * L <= 2^31 - 256.  Pointers need the alignment of their element type (16-byte
  * aligned tensors with groups of whole 16-byte pieces take a vectorised path).
  * Outputs may not alias inputs.  Asynchronous on `stream`.
  * Errors: MDN_ERR_INVALID_ARG, MDN_ERR_UNSUPPORTED, MDN_ERR_CUDA.

@@ -966,6 +966,7 @@ mdn_status check(int N, int L, int C, int G, mdn_dtype dt, int act)
     if (dt != MDN_F32 && dt != MDN_BF16) return MDN_ERR_UNSUPPORTED;
     // grid limits: rows and their groups per call, row blocks' second dimension
     if ((long long)N * G >= (1LL << 30) || C >= (1 << 22)) return MDN_ERR_UNSUPPORTED;
+    if (L > 0x7fffff00) return MDN_ERR_UNSUPPORTED;  // row indices run a batch past L
     if (L > 1 && G > 8 * 65535) return MDN_ERR_UNSUPPORTED;  // 8 groups to a block of the rows form
     if (N > 65535) {  // only the tokens form takes more
         const Plan p = plan_of(N, L, C, G, dt == MDN_F32, true, true);

@@ -145,6 +145,7 @@ def test_group_norm_refusals(lib):
     assert fw(N=1 << 17, L=2) == E.MDN_ERR_UNSUPPORTED
     assert fw(C=1 << 22, G=1) == E.MDN_ERR_UNSUPPORTED
     assert fw(C=1 << 20, G=1 << 20, N=1, L=2) == E.MDN_ERR_UNSUPPORTED
+    assert fw(C=1, G=1, N=1, L=(1 << 31) - 4) == E.MDN_ERR_UNSUPPORTED
     assert fw(N=0, x=None) == E.MDN_OK and fw(L=0, x=None) == E.MDN_OK
 
     def bw(dy=FAKE, dx=FAKE, gate=None, dg=None, w=FAKE, dw=FAKE, db=FAKE, ws=FAKE, wsb=1 << 30,

@@ -453,8 +453,9 @@ mdn_status mdn_chunk_fwd_noalloc(const void *q, const void *k, const void *v,
  * fp32 for the whole sequence.  Support: d_k = d_v in {64, 128}, C = 64, fp32
  * or bf16.
  *
- * bf16 chunk calls work on 64 tokens of a sequence at a time (forward d 64 and
- * 128, backward d 128): there a value that is not finite reaches every token of
+ * bf16 chunk calls work on 64 tokens of a sequence at a time (forward d 64 with
+ * more than 64 tokens, d 128 with more than 32; backward d 128 with more than
+ * 16; of a packed call all its tokens count): there a value that is not finite reaches every token of
  * its 64, the earlier ones too, and all after them.  alpha_log below -1e4
  * counts as -1e4 (alpha is 0 in fp32 from -104 on).
  */

@@ -23,8 +23,13 @@ struct Sizes {
     mdn_dtype dt;
     bool packed;
     int flags;
-    bool tc() const { return dt == MDN_BF16 && !(flags & MDN_FORCE_SIMT); }
-    bool bwd_tc() const { return tc() && dk == 128; }
+    // On the tensor cores?  Sequences of less than a chunk or so are cheaper token by token (and
+    // exact in fp32).  Measured, one and 1024 chains of d 128, tensor cores and CUDA cores, us:
+    // forward 16 tokens 25 and 10, 131 and 84; 32: 23 and 13, 133 and 144; 64: 21 and 18, 136
+    // and 264; backward 16 tokens 48 and 40, 307 and 289; 32: 48 and 64, 311 and 491.  Forward,
+    // d 64, 64 tokens: 21 and 16, 105 and 90.  Of a packed call only the sum is known.
+    bool bf16() const { return dt == MDN_BF16 && !(flags & MDN_FORCE_SIMT); }
+    bool tc(bool bwd) const { return bf16() && (bwd ? dk == 128 && T > 16 : T > 4096 / dk); }
     long long rows() const { return packed ? T : (long long)B * T; }
     // chunks of the call: every sequence ends in at most one partial chunk
     long long chunks() const
@@ -62,7 +67,7 @@ Layout layout(const Sizes& z, bool bwd)
     // status words first (mdn_chunk_fwd_status reads them there), then the ready flags and the
     // work counter of the operand blocks: one memset clears both
     size_t off = 64;
-    if (z.tc()) off += ((size_t)z.chunks() * z.H + 2) * sizeof(unsigned);
+    if (z.tc(bwd)) off += ((size_t)z.chunks() * z.H + 2) * sizeof(unsigned);
     w.head = off;
     off = align_up(off);
     if (z.packed) {
@@ -71,10 +76,10 @@ Layout layout(const Sizes& z, bool bwd)
         w.seq_order = off;   off += align_up((size_t)z.B * sizeof(int));
         w.chunk_order = off; off += align_up((size_t)z.chunks() * sizeof(int));
     }
-    if (!bwd && z.tc()) {
+    if (!bwd && z.tc(false)) {
         w.blk = off; off += align_up((size_t)z.chunks() * z.H * gdr::kBlkBytes);
     }
-    if (bwd && z.bwd_tc()) {
+    if (bwd && z.tc(true)) {
         const size_t ch = (size_t)z.chunks() * z.H, dd = (size_t)z.dk * z.dv;
         // 32 columns a slice while four CTAs per chain fit a B200's 148 SMs at once (the
         // shortest chunk step), else 64 (half the loads of K, Q and the images)
@@ -118,7 +123,7 @@ mdn_status begin(gdr::Args& a, const Sizes& z, const Layout& w, char* ws, const 
     a.B = z.B; a.T = z.T; a.Hk = z.Hk; a.H = z.H; a.D = z.dk;
     a.NT = (int)(z.packed ? z.chunks() : ((long long)z.T + z.C - 1) / z.C);
     a.status = reinterpret_cast<unsigned*>(ws + w.status);
-    if (z.tc()) a.ready = a.status + 16;
+    if (w.head > 64) a.ready = a.status + 16;
     cudaError_t e = cudaMemsetAsync(a.status, 0, w.head, s);
     if (e != cudaSuccess) return cuda_fail(e);
     if (!z.packed) return MDN_OK;
@@ -234,7 +239,7 @@ mdn_status fwd_impl(const Sizes& z, const void* q, const void* k, const void* v,
     if ((st = begin(a, z, w, ws, cu_seqlens, s)) != MDN_OK) return st;
     if ((flags & MDN_ZERO_BEHIND) && (st = zero_behind(rest, a.cu_s, z, s)) != MDN_OK) return st;
     // no tokens: S_T = S0, which the CUDA-core kernel's walk over nothing gives
-    const cudaError_t e = z.tc() && z.rows() > 0 ? gdr::launch_fwd_tc(a, s) : gdr::launch_fwd_simt(a, z.dt, s);
+    const cudaError_t e = z.tc(false) ? gdr::launch_fwd_tc(a, s) : gdr::launch_fwd_simt(a, z.dt, s);
     if (e != cudaSuccess) return cuda_fail(e);
     if (!(flags & MDN_CHECK_FINITE)) return MDN_OK;
     const bool bf = z.dt == MDN_BF16;
@@ -292,7 +297,7 @@ mdn_status bwd_impl(const Sizes& z, const void* q, const void* k, const float* a
     if ((st = begin(a, z, w, ws, cu_seqlens, s)) != MDN_OK) return st;
     if ((flags & MDN_ZERO_BEHIND) && (st = zero_behind(rest, a.cu_s, z, s)) != MDN_OK) return st;
     // no tokens: dS0 = dS_T, which the CUDA-core chain's walk over nothing gives
-    const bool tc = z.bwd_tc() && z.rows() > 0;
+    const bool tc = z.tc(true);
     cudaError_t e = tc ? gdr::launch_bwd_tc(a, s) : gdr::launch_bwd_simt(a, z.dt, s);
     if (e == cudaSuccess && a.dqp) e = gdr::launch_fold_heads(a, z.dt, s);
     if (e != cudaSuccess) return cuda_fail(e);

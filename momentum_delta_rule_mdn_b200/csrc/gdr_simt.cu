@@ -987,8 +987,10 @@ cudaError_t run(K kernel, long long blocks, int threads, size_t shm, cudaStream_
 // waiting.  At d 64 a token takes 0.17 us in the forward pass and 0.15 in the reverse
 // chain, the states beside it (0.20, 0.23 and 0.09 for the states with a reduction per
 // token and 32 columns a CTA); bound by a warp's own latency, 3.6 cycles an instruction
-// with one warp per scheduler.  More chains: the whole head a CTA and four columns a thread, which reads each
-// staged k and q once for four columns.
+// with one warp per scheduler.  More chains: the whole head a CTA and four columns a
+// thread, which reads each staged k and q once for four columns.  At the border, 256
+// tokens forward: 74 chains of d 128 take 183 us (whole heads 218), 148 of d 64 92 us (86;
+// in bf16 82 and 94).
 template <typename T, int D>
 cudaError_t fwd_typed(const Args& a, cudaStream_t s)
 {

@@ -149,6 +149,30 @@ def test_new_outputs_are_zero_behind_the_last_sequence(H, Hk, off, dtype):
         assert torch.isfinite(t).all() and (off[-1] == 0 or t[1:off[-1]].ne(0).any())
 
 
+@pytest.mark.parametrize("T", [1, 3, 4, 5, 16, 17, 32, 33, 64, 65])
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("d,H,Hk", [(128, 6, 2), (64, 5, 5)])
+def test_few_tokens(d, H, Hk, packed, T):
+    """Lengths at which bf16 calls change between the CUDA cores and the tensor cores."""
+    x = R.inputs(1, T, H, Hk, d, BF16, seed=T + 20)
+    n = ("q", "k", "v", "alpha_log", "beta", "S0", "do", "dS_T")
+    q, k, v, al, be, S0, do, dST = (x[i].cuda() if x[i] is not None else None for i in n)
+    if packed:
+        cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+        o, vt, S = mdn.gdr_chunk_fwd_varlen(q[0], k[0], v[0], al[0], be[0], cu, None, S0)
+        g = mdn.gdr_chunk_bwd_varlen(q[0], k[0], al[0], be[0], cu, None, vt, do[0], S0, dST)
+        got = dict(o=o[None], vt=vt[None], S=S) | {i: t if i == "dS0" else t[None] for i, t in g.items()}
+    else:
+        o, vt, S = mdn.gdr_chunk_fwd(q, k, v, al, be, None, S0)
+        got = dict(o=o, vt=vt, S=S) | mdn.gdr_chunk_bwd(q, k, al, be, None, vt, do, S0, dST)
+    ref = dict(zip(("o", "vt", "S"), R.fwd(*[x[i] for i in n[:5]], d ** -0.5, x["S0"])))
+    ref |= R.bwd(x["q"], x["k"], x["alpha_log"], x["beta"], d ** -0.5, got["vt"].cpu(), x["do"], x["S0"],
+                 x["dS_T"])
+    tol = {F32: 2e-5, BF16: 4.5e-3}
+    for i, r in ref.items():
+        assert R.rel(got[i], r) <= tol[got[i].dtype], i
+
+
 @pytest.mark.parametrize("flags", [0, E.MDN_FORCE_SIMT])
 @pytest.mark.parametrize("dtype,d", [(BF16, 128), (BF16, 64), (F32, 64)])
 def test_minus_infinity_resets(dtype, d, flags):

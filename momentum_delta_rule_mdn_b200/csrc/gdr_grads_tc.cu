@@ -197,7 +197,6 @@ grads_kernel(const __grid_constant__ GradMaps tm, const Args a, const long long 
     int u = 0;  // heads processed: the phase of their barriers
     for (int it = 0; cur.cr.valid > 0; ++it) {
         const ChunkRows cr = cur.cr;
-        const long long n = cur.n;
         const int hk = cur.hk;
         const Item nx = item(blockIdx.x + (long long)(it + 1) * gridDim.x);
         if (a.cu_s && cr.valid < kChunk) {

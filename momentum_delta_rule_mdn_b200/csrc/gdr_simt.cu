@@ -730,9 +730,7 @@ __global__ void __launch_bounds__(NC * RL) back_few_kernel(const Args a)
 // The token gradients of one chunk of one head, from the S entering it and
 // the adjoint of the S leaving it: rows of S and of G are independent here, so
 // a thread holds 4 rows and every eighth float4 of columns.  Forward over the
-// tokens for dq and alpha S dv, backward for G vtilde.  dalpha_log follows
-// from   dalpha_log_t = dalpha_log_{t+1} + q.dq - beta dbeta - alpha k.(S dv),
-// started at the chunk's end with <G, S>, so that sums stay inside a chunk.
+// tokens for dq and alpha S dv, backward for G vtilde.
 template <typename T, int D>
 __global__ void __launch_bounds__(D * 2, D == 64 ? 4 : 2) token_grads_kernel(const Args a)
 {
@@ -742,8 +740,7 @@ __global__ void __launch_bounds__(D * 2, D == 64 ? 4 : 2) token_grads_kernel(con
     const Buffers<float, TB, D> fbuf{reinterpret_cast<float*>(shm + kChunk * D * 4)};  // dv
     const Buffers<T, TB, 4 * D> buf{reinterpret_cast<T*>(shm + (kChunk + 2 * TB) * D * 4)};  // do, vtilde, k, q
     __shared__ float al[TB], be[TB], dd[TB];
-    __shared__ float cc[kChunk][NW], bb[kChunk][NW];  // a warp's share of q.dq - k.(alpha S dv); dbeta
-    __shared__ float ip[NW];
+    __shared__ float bb[kChunk][NW];  // a warp's share of dbeta
     const long long n = blockIdx.x / a.H;
     const int h = blockIdx.x % a.H, hk = h / (a.H / a.Hk);
     const ChunkRows cr = chunk_rows(a, n);
@@ -827,34 +824,16 @@ __global__ void __launch_bounds__(D * 2, D == 64 ? 4 : 2) token_grads_kernel(con
             // lane r: dq of row r; lane 4 + r: alpha S dv of row r
             const float x = alpha * lanes_sum8(p, rl);
             const int row = row4 + rl % 4;
-            const float kv = ld_elem(ks + t * D + row), qv = ld_elem(qs + t * D + row);
+            const float kv = ld_elem(ks + t * D + row);
             const size_t tok = (size_t)(cr.row0 + t0 + t);
-            float share;
             if (rl < 4) {
                 const float y = a.scale * fmaf(b * kv, dd[t], x);
-                share = qv * y;
                 if (a.dqp) a.dqp[(tok * a.H + h) * D + row] = y;
                 else st_elem(static_cast<T*>(a.dq) + (tok * a.Hk + hk) * D + row, y);
             } else {
-                share = -kv * x;
                 dks[t0 + t][row] = x;
             }
-            share = warp_sum(share);
-            if (lane == 0) cc[t0 + t][warp] = share;
         }
-    }
-    // <G, S> at the chunk's end, then G
-    {
-        float x = 0.f;
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float4 g4 = *reinterpret_cast<const float4*>(a.GG + sbase + r * D + i * (4 * RL) + rl * 4);
-                x = dot4(g4, make_float4(s[r][4 * i], s[r][4 * i + 1], s[r][4 * i + 2], s[r][4 * i + 3]), x);
-            }
-        x = warp_sum(x);
-        if (lane == 0) ip[warp] = x;
     }
     load(a.GG);
     for (int t0 = top; t0 >= 0; t0 -= TB, ++blk) {
@@ -903,41 +882,139 @@ __global__ void __launch_bounds__(D * 2, D == 64 ? 4 : 2) token_grads_kernel(con
         }
     }
     __syncthreads();
-    // warp 0: dbeta, and dalpha_log as a suffix sum over the chunk's tokens
-    if (warp == 0) {
-        float c[2], b[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int t = 2 * lane + e;
-            c[e] = b[e] = 0.f;
-            if (t < cr.valid) {
-                const size_t at = (size_t)(cr.row0 + t) * a.H + h;
-                for (int w = 0; w < NW; ++w) {
-                    c[e] += cc[t][w];
-                    b[e] += bb[t][w];
+    for (int t = tid; t < cr.valid; t += NTH) {
+        float b = 0.f;
+        for (int w = 0; w < NW; ++w) b += bb[t][w];
+        a.dbeta[(size_t)(cr.row0 + t) * a.H + h] = b;
+    }
+}
+
+// dalpha_log of one chunk of one head: the sum of everything whose decay spans the token.
+// With S entering and G leaving the chunk and L_{r,i} the decay from token i to token r,
+//     Z_{r,i} = L_{r,i} beta_i (scale (do_r.vtilde_i) (q_r.k_i) - (dv_r.vtilde_i) (k_r.k_i)),  i < r,
+//     e_r = L_{r,0} (scale q_r^T S do_r - k_r^T S dv_r),   f_i = L_{end,i} beta_i k_i^T G vtilde_i,
+//     dalpha_log_t = L_{end,0} <G, S> + sum_{r >= t} e_r + sum_{i < t} f_i + sum_{r >= t > i} Z_{r,i}.
+// (The recurrence dalpha_log_t = dalpha_log_{t+1} + q.dq - beta dbeta - ... needs no pairs, but
+// adds and later takes off what each token does to itself, larger by 1 / alpha than what is
+// left: at alpha = e^-8 it lost 1e-3 of the result.)  Four threads a token; decays are running
+// products, sums have a fixed order.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) dalpha_kernel(const Args a)
+{
+    constexpr int LD = D + 4, P = D / 4;  // P: a thread's columns
+    extern __shared__ __align__(16) uint8_t shm[];
+    float* ks = reinterpret_cast<float*>(shm);  // [64][LD] each
+    float* qs = ks + kChunk * LD;
+    float* vs = qs + kChunk * LD;
+    float* os = vs + kChunk * LD;
+    float* ds = os + kChunk * LD;
+    float (*z)[kChunk + 1] = reinterpret_cast<float (*)[kChunk + 1]>(ds + kChunk * LD);
+    __shared__ float al[kChunk], be[kChunk], e_[kChunk], f_[kChunk], rc[kChunk], gsum[8];
+    const long long n = blockIdx.x / a.H;
+    const int h = blockIdx.x % a.H, hk = h / (a.H / a.Hk);
+    const ChunkRows cr = chunk_rows(a, n);
+    if (cr.valid <= 0) return;
+    const int tid = threadIdx.x, r = tid / 4, part = tid % 4;
+    for (int x = tid; x < kChunk * (D / 4); x += 256) {
+        const int t = x / (D / 4), c = x % (D / 4) * 4;
+        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+        const bool in = t < cr.valid;
+        const size_t kt = ((size_t)(cr.row0 + (in ? t : 0)) * a.Hk + hk) * D + c;
+        const size_t vt = ((size_t)(cr.row0 + (in ? t : 0)) * a.H + h) * D + c;
+        *reinterpret_cast<float4*>(ks + t * LD + c) = in ? get4(static_cast<const T*>(a.k) + kt) : zero;
+        *reinterpret_cast<float4*>(qs + t * LD + c) = in ? get4(static_cast<const T*>(a.q) + kt) : zero;
+        *reinterpret_cast<float4*>(vs + t * LD + c) = in ? get4(static_cast<const T*>(a.vt) + vt) : zero;
+        *reinterpret_cast<float4*>(os + t * LD + c) = in ? get4(static_cast<const T*>(a.d_o) + vt) : zero;
+        *reinterpret_cast<float4*>(ds + t * LD + c) = in ? get4(a.dvf + vt) : zero;
+    }
+    if (tid < kChunk) {
+        const bool in = tid < cr.valid;
+        const size_t at = (size_t)(cr.row0 + (in ? tid : 0)) * a.H + h;
+        al[tid] = in ? expf(a.alpha_log[at]) : 1.f;
+        be[tid] = in ? a.beta[at] : 0.f;
+    }
+    __syncthreads();
+    auto sum4 = [](float x) {
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        return x + __shfl_xor_sync(0xffffffffu, x, 2);
+    };
+    // pairs: this thread's token is i, r walks behind it; columns 4 part + 16 c of the rows
+    {
+        const int i = r;
+        float L = 1.f;
+        for (int t = 0; t < kChunk; ++t) {
+            float ov = 0.f, dv = 0.f, qk = 0.f, kk = 0.f;
+            if (t > i) {
+                L *= al[t];
+#pragma unroll 4
+                for (int c = 4 * part; c < D; c += 16) {
+                    const float4 vi = get4(vs + i * LD + c), ki = get4(ks + i * LD + c);
+                    ov = dot4(get4(os + t * LD + c), vi, ov);
+                    dv = dot4(get4(ds + t * LD + c), vi, dv);
+                    qk = dot4(get4(qs + t * LD + c), ki, qk);
+                    kk = dot4(get4(ks + t * LD + c), ki, kk);
                 }
-                c[e] = fmaf(-a.beta[at], b[e], c[e]);
-                a.dbeta[at] = b[e];
             }
+            ov = sum4(ov); dv = sum4(dv); qk = sum4(qk); kk = sum4(kk);
+            if (part == 0) z[t][i] = t > i ? L * be[i] * (a.scale * ov * qk - dv * kk) : 0.f;
         }
-        float end = 0.f;
-        for (int w = 0; w < NW; ++w) end += ip[w];
-        float x = c[0] + c[1];  // inclusive suffix sum over lanes
+        // S and G against this thread's token
+        const float* S = a.SS + ((size_t)n * a.H + h) * D * D;
+        const float* G = a.GG + ((size_t)n * a.H + h) * D * D;
+        float o[P], d[P], v[P], es = 0.f, fs = 0.f;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const float y = __shfl_down_sync(0xffffffffu, x, off);
-            if (lane + off < 32) x += y;
+        for (int c = 0; c < P; ++c) {
+            const int y = 4 * part + c % 4 + c / 4 * 16;
+            o[c] = a.scale * os[r * LD + y];
+            d[c] = ds[r * LD + y];
+            v[c] = vs[r * LD + y];
         }
+        for (int x = 0; x < D; ++x) {
+            float so = 0.f, sd = 0.f, gv = 0.f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int t = 2 * lane + e;
-            if (t < cr.valid) {
-                float y = (e == 0 ? x : x - c[0]) + end;
-                // nothing enters a sequence's first token from no state: its decay has no effect
-                if (t == 0 && cr.first && !a.S0) y = 0.f;
-                a.dalpha_log[(size_t)(cr.row0 + t) * a.H + h] = y;
+            for (int c = 0; c < P; c += 4) {
+                const float4 s4 = *reinterpret_cast<const float4*>(S + (size_t)x * D + 4 * part + c * 4);
+                const float4 g4 = *reinterpret_cast<const float4*>(G + (size_t)x * D + 4 * part + c * 4);
+                so = dot4(s4, make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]), so);
+                sd = dot4(s4, make_float4(d[c], d[c + 1], d[c + 2], d[c + 3]), sd);
+                gv = dot4(g4, make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]), gv);
             }
+            es += qs[r * LD + x] * so - ks[r * LD + x] * sd;
+            fs = fmaf(ks[r * LD + x], gv, fs);
         }
+        es = sum4(es);
+        fs = sum4(fs);
+        float before = 1.f, after = 1.f;
+        for (int t = 0; t < kChunk; ++t) {
+            if (t <= r) before *= al[t];
+            else after *= al[t];
+        }
+        if (part == 0) {
+            e_[r] = before * es;
+            f_[r] = after * be[r] * fs;
+        }
+        float gs = 0.f;
+        for (int x = tid; x < D * D / 4; x += 256)
+            gs = dot4(*reinterpret_cast<const float4*>(S + 4 * x), *reinterpret_cast<const float4*>(G + 4 * x), gs);
+        gs = warp_sum(gs);
+        if (tid % 32 == 0) gsum[tid / 32] = before * after * gs;
+    }
+    __syncthreads();
+    {   // row sums minus column sums of Z
+        float x = 0.f;
+        for (int c = part; c < kChunk; c += 4) x += z[r][c] - z[c][r];
+        x = sum4(x);
+        if (part == 0) rc[r] = x;
+    }
+    __syncthreads();
+    if (tid < cr.valid) {
+        float y = 0.f;
+        for (int w = 0; w < 8; ++w) y += gsum[w];
+        for (int t = 0; t < tid; ++t) y += f_[t];
+        float x = 0.f;
+        for (int t = kChunk - 1; t >= tid; --t) x += e_[t] + rc[t];
+        // nothing enters a sequence's first token from no state: its decay has no effect
+        a.dalpha_log[(size_t)(cr.row0 + tid) * a.H + h] = tid == 0 && cr.first && !a.S0 ? 0.f : x + y;
     }
 }
 
@@ -1023,8 +1100,11 @@ cudaError_t bwd_typed(const Args& a, cudaStream_t s)
     const long long blocks = chunks(a) * a.H;
     if (blocks == 0) return cudaSuccess;
     ProfScope ps(kGdrBwdGrads, s);
-    return run(token_grads_kernel<T, D>, blocks, 2 * D,
-               (kChunk + 2 * kGradTokens) * D * sizeof(float) + 2 * kGradTokens * 4 * D * sizeof(T), s, a);
+    e = run(token_grads_kernel<T, D>, blocks, 2 * D,
+            (kChunk + 2 * kGradTokens) * D * sizeof(float) + 2 * kGradTokens * 4 * D * sizeof(T), s, a);
+    if (e != cudaSuccess) return e;
+    return run(dalpha_kernel<T, D>, blocks, 256,
+               (5 * kChunk * (D + 4) + kChunk * (kChunk + 1)) * sizeof(float), s, a);
 }
 
 }  // namespace

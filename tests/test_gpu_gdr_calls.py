@@ -195,6 +195,22 @@ def test_minus_infinity_resets(dtype, d, flags):
             assert R.rel(got[i], r) <= tol[got[i].dtype], i
 
 
+@pytest.mark.parametrize("dtype,d,flags", [(F32, 64, 0), (F32, 128, 0), (BF16, 64, 0), (BF16, 128, 0),
+                                           (BF16, 128, E.MDN_FORCE_SIMT)])
+@pytest.mark.parametrize("decay", [3.0, 8.0])
+def test_strong_decay_keeps_the_gates_gradients(decay, dtype, d, flags):
+    """alpha of e^-3 and e^-8: what a token's decay acts on is a small rest beside what the token
+    writes itself."""
+    x = R.inputs(1, 200, 2, 2, d, dtype, seed=5, decay=decay)
+    q, k, v, al, be, S0, do, dST = (x[i].cuda() if x[i] is not None else None
+                                    for i in ("q", "k", "v", "alpha_log", "beta", "S0", "do", "dS_T"))
+    vt = mdn.gdr_chunk_fwd(q, k, v, al, be, None, S0, flags=flags)[1]
+    g = mdn.gdr_chunk_bwd(q, k, al, be, None, vt, do, S0, dST, flags=flags)
+    r = R.bwd(x["q"], x["k"], x["alpha_log"], x["beta"], d ** -0.5, vt.cpu(), x["do"], x["S0"], x["dS_T"])
+    for i in ("dalpha_log", "dbeta", "dS0"):
+        assert R.rel(g[i], r[i]) <= 2e-5, i
+
+
 @pytest.mark.parametrize("dtype,d", [(BF16, 128), (F32, 64)])
 def test_a_sequence_that_is_not_finite_stays_alone(dtype, d):
     """Packed neighbours, in the same 64-token tile of the buffer, are not reached."""

@@ -942,19 +942,26 @@ __global__ void __launch_bounds__(256) dalpha_kernel(const Args a)
     {
         const int i = r;
         float L = 1.f;
-        for (int t = 0; t < kChunk; ++t) {
+        float4 vi[P / 4], ki[P / 4];
+#pragma unroll
+        for (int c = 0; c < P / 4; ++c) {
+            vi[c] = get4(vs + i * LD + 4 * part + 16 * c);
+            ki[c] = get4(ks + i * LD + 4 * part + 16 * c);
+        }
+        const int first = tid / 32 * 8 + 1;  // the warp's first token but one
+        for (int t = part; t < first; t += 4) z[t][i] = 0.f;
+#pragma unroll 2
+        for (int t = first; t < kChunk; ++t) {
             float ov = 0.f, dv = 0.f, qk = 0.f, kk = 0.f;
-            if (t > i) {
-                L *= al[t];
-#pragma unroll 4
-                for (int c = 4 * part; c < D; c += 16) {
-                    const float4 vi = get4(vs + i * LD + c), ki = get4(ks + i * LD + c);
-                    ov = dot4(get4(os + t * LD + c), vi, ov);
-                    dv = dot4(get4(ds + t * LD + c), vi, dv);
-                    qk = dot4(get4(qs + t * LD + c), ki, qk);
-                    kk = dot4(get4(ks + t * LD + c), ki, kk);
-                }
+#pragma unroll
+            for (int c = 0; c < P / 4; ++c) {
+                const int at = t * LD + 4 * part + 16 * c;
+                ov = dot4(get4(os + at), vi[c], ov);
+                dv = dot4(get4(ds + at), vi[c], dv);
+                qk = dot4(get4(qs + at), ki[c], qk);
+                kk = dot4(get4(ks + at), ki[c], kk);
             }
+            if (t > i) L *= al[t];
             ov = sum4(ov); dv = sum4(dv); qk = sum4(qk); kk = sum4(kk);
             if (part == 0) z[t][i] = t > i ? L * be[i] * (a.scale * ov * qk - dv * kk) : 0.f;
         }
@@ -969,6 +976,7 @@ __global__ void __launch_bounds__(256) dalpha_kernel(const Args a)
             d[c] = ds[r * LD + y];
             v[c] = vs[r * LD + y];
         }
+#pragma unroll 2
         for (int x = 0; x < D; ++x) {
             float so = 0.f, sd = 0.f, gv = 0.f;
 #pragma unroll

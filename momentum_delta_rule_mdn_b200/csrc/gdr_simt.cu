@@ -897,7 +897,7 @@ __global__ void __launch_bounds__(D * 2, D == 64 ? 4 : 2) token_grads_kernel(con
 // (The recurrence dalpha_log_t = dalpha_log_{t+1} + q.dq - beta dbeta - ... needs no pairs, but
 // adds and later takes off what each token does to itself, larger by 1 / alpha than what is
 // left: at alpha = e^-8 it lost 1e-3 of the result.)  Four threads a token; decays are running
-// products, sums have a fixed order.
+// products, sums have a fixed order.  Bound by latency: 264 chunks of d 64 take 50 us.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) dalpha_kernel(const Args a)
 {
@@ -938,6 +938,70 @@ __global__ void __launch_bounds__(256) dalpha_kernel(const Args a)
         x += __shfl_xor_sync(0xffffffffu, x, 1);
         return x + __shfl_xor_sync(0xffffffffu, x, 2);
     };
+    {
+        // S and G against this thread's token
+        const float* S = a.SS + ((size_t)n * a.H + h) * D * D;
+        const float* G = a.GG + ((size_t)n * a.H + h) * D * D;
+        float o[P], d[P], v[P], es = 0.f, fs = 0.f;
+#pragma unroll
+        for (int c = 0; c < P; ++c) {
+            const int y = 4 * part + c % 4 + c / 4 * 16;
+            o[c] = a.scale * os[r * LD + y];
+            d[c] = ds[r * LD + y];
+            v[c] = vs[r * LD + y];
+        }
+        // 16 rows of both at a time through shared memory (where Z goes later), the next ones
+        // on their way
+        constexpr int TR = 16, NL = 2 * TR * D / 4 / 256;
+        float* st = &z[0][0];
+        static_assert(2 * TR * D <= kChunk * (kChunk + 1), "tile");
+        float4 nx[NL];
+        auto ahead = [&](int x0) {
+#pragma unroll
+            for (int l = 0; l < NL; ++l) {
+                const int e = tid + 256 * l, of = e % (TR * D / 4) * 4;
+                nx[l] = get4((e < TR * D / 4 ? S : G) + (size_t)x0 * D + of);
+            }
+        };
+        ahead(0);
+        float gs = 0.f;
+        for (int x0 = 0; x0 < D; x0 += TR) {
+            __syncthreads();
+#pragma unroll
+            for (int l = 0; l < NL; ++l) *reinterpret_cast<float4*>(st + 4 * (tid + 256 * l)) = nx[l];
+            __syncthreads();
+            if (x0 + TR < D) ahead(x0 + TR);
+            for (int e = tid; e < TR * D / 4; e += 256) gs = dot4(get4(st + 4 * e), get4(st + TR * D + 4 * e), gs);
+#pragma unroll 2
+            for (int x = x0; x < x0 + TR; ++x) {
+                float so = 0.f, sd = 0.f, gv = 0.f;
+#pragma unroll
+                for (int c = 0; c < P; c += 4) {
+                    const float4 s4 = get4(st + (x - x0) * D + 4 * part + c * 4);
+                    const float4 g4 = get4(st + TR * D + (x - x0) * D + 4 * part + c * 4);
+                    so = dot4(s4, make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]), so);
+                    sd = dot4(s4, make_float4(d[c], d[c + 1], d[c + 2], d[c + 3]), sd);
+                    gv = dot4(g4, make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]), gv);
+                }
+                es += qs[r * LD + x] * so - ks[r * LD + x] * sd;
+                fs = fmaf(ks[r * LD + x], gv, fs);
+            }
+        }
+        es = sum4(es);
+        fs = sum4(fs);
+        float before = 1.f, after = 1.f;
+        for (int t = 0; t < kChunk; ++t) {
+            if (t <= r) before *= al[t];
+            else after *= al[t];
+        }
+        if (part == 0) {
+            e_[r] = before * es;
+            f_[r] = after * be[r] * fs;
+        }
+        gs = warp_sum(gs);
+        if (tid % 32 == 0) gsum[tid / 32] = before * after * gs;
+    }
+    __syncthreads();
     // pairs: this thread's token is i, r walks behind it; columns 4 part + 16 c of the rows
     {
         const int i = r;
@@ -965,47 +1029,6 @@ __global__ void __launch_bounds__(256) dalpha_kernel(const Args a)
             ov = sum4(ov); dv = sum4(dv); qk = sum4(qk); kk = sum4(kk);
             if (part == 0) z[t][i] = t > i ? L * be[i] * (a.scale * ov * qk - dv * kk) : 0.f;
         }
-        // S and G against this thread's token
-        const float* S = a.SS + ((size_t)n * a.H + h) * D * D;
-        const float* G = a.GG + ((size_t)n * a.H + h) * D * D;
-        float o[P], d[P], v[P], es = 0.f, fs = 0.f;
-#pragma unroll
-        for (int c = 0; c < P; ++c) {
-            const int y = 4 * part + c % 4 + c / 4 * 16;
-            o[c] = a.scale * os[r * LD + y];
-            d[c] = ds[r * LD + y];
-            v[c] = vs[r * LD + y];
-        }
-#pragma unroll 2
-        for (int x = 0; x < D; ++x) {
-            float so = 0.f, sd = 0.f, gv = 0.f;
-#pragma unroll
-            for (int c = 0; c < P; c += 4) {
-                const float4 s4 = *reinterpret_cast<const float4*>(S + (size_t)x * D + 4 * part + c * 4);
-                const float4 g4 = *reinterpret_cast<const float4*>(G + (size_t)x * D + 4 * part + c * 4);
-                so = dot4(s4, make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]), so);
-                sd = dot4(s4, make_float4(d[c], d[c + 1], d[c + 2], d[c + 3]), sd);
-                gv = dot4(g4, make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]), gv);
-            }
-            es += qs[r * LD + x] * so - ks[r * LD + x] * sd;
-            fs = fmaf(ks[r * LD + x], gv, fs);
-        }
-        es = sum4(es);
-        fs = sum4(fs);
-        float before = 1.f, after = 1.f;
-        for (int t = 0; t < kChunk; ++t) {
-            if (t <= r) before *= al[t];
-            else after *= al[t];
-        }
-        if (part == 0) {
-            e_[r] = before * es;
-            f_[r] = after * be[r] * fs;
-        }
-        float gs = 0.f;
-        for (int x = tid; x < D * D / 4; x += 256)
-            gs = dot4(*reinterpret_cast<const float4*>(S + 4 * x), *reinterpret_cast<const float4*>(G + 4 * x), gs);
-        gs = warp_sum(gs);
-        if (tid % 32 == 0) gsum[tid / 32] = before * after * gs;
     }
     __syncthreads();
     {   // row sums minus column sums of Z

@@ -17,11 +17,12 @@
 //    of rows is read by whole rows, each thread keeping its channels; partial
 //    statistics per block go through the workspace, then a second pass reads
 //    the rows again (from L2 while a call's tensors fit there).
-// Statistics are fp32 and never a difference of large sums: the tokens form
-// takes the variance about the mean from registers, the rows form sums about
-// each thread's first value and joins (count, mean, M2) triples.  dw and db are
-// summed per thread, per block and then over blocks in a fixed order, so
-// results do not depend on timing.
+// The tokens form takes the variance in fp32 about the mean, from registers.  The
+// rows form sums a block's values and their squares in fp64 (an fp32 sum of squares
+// about any one value loses the variance when that value lies far from the rest),
+// keeps a block's (mean, sum of squared distances) in fp32 and joins those about
+// the group's mean.  dw and db are summed per thread, per block and then over
+// blocks in a fixed order, so results do not depend on timing.
 #include <algorithm>
 #include <type_traits>
 
@@ -534,18 +535,6 @@ __device__ __forceinline__ RowBlock row_block(const Args& a)
     return r;
 }
 
-// (count, mean, M2) of two sets joined into the first.
-__device__ __forceinline__ void join(float& k, float& mean, float& m2, float k2, float e2, float q2)
-{
-    const float t = k + k2, d = e2 - mean;
-    if (t > 0.f) {
-        const float f = k2 / t;
-        m2 += q2 + d * d * k * f;
-        mean += d * f;
-    }
-    k = t;
-}
-
 // Partial statistics.  One warp per (n, group, row block): the lanes take the
 // group's values of the block in turn.
 template <typename T, bool BWD, int ACT, bool GATE>
@@ -563,43 +552,40 @@ __global__ void __launch_bounds__(kThreads) rows_part_kernel(const Args a)
     // lane's first value and the step from value to value, as (row, channel)
     int r = lane / Cg, c = lane % Cg;
     const int sr = 32 / Cg, sc = 32 % Cg;
-    float p = 0.f, q = 0.f;
     float* out = a.part + (((size_t)n * a.blocks + blockIdx.x) * a.G + g) * 2;
     if constexpr (!BWD) {
-        const float shift = cnt > 0 ? ld_elem(x + base) : 0.f;  // the block's first value
+        // Q - P mean keeps 53 - 2 log2(|mean| / spread) bits: 24 of them at a mean of 2^14 spreads
+        double p = 0.0, q = 0.0;
         for (long long i = lane; i < cnt; i += 32 * kBatch) {
             float v[kBatch];
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
-                v[u] = i + 32 * u < cnt ? ld_elem(x + base + (size_t)r * a.C + c) - shift : 0.f;
+                v[u] = i + 32 * u < cnt ? ld_elem(x + base + (size_t)r * a.C + c) : 0.f;
                 r += sr; c += sc;
                 if (c >= Cg) { c -= Cg; ++r; }
             }
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
-                p += v[u];
-                q = fmaf(v[u], v[u], q);
+                const double w = v[u];
+                p += w;
+                q = fma(w, w, q);
             }
         }
-        // (mean, M2) of the lane's values, joined pairwise over the lanes
-        float k = (float)((cnt - lane + 31) / 32);
-        if (cnt <= lane) k = 0.f;
-        float mean = k > 0.f ? p / k : 0.f, m2 = k > 0.f ? q - p * mean : 0.f;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const float k2 = __shfl_xor_sync(0xffffffffu, k, off);
-            const float e2 = __shfl_xor_sync(0xffffffffu, mean, off);
-            const float q2 = __shfl_xor_sync(0xffffffffu, m2, off);
-            join(k, mean, m2, k2, e2, q2);
+            p += __shfl_xor_sync(0xffffffffu, p, off);
+            q += __shfl_xor_sync(0xffffffffu, q, off);
         }
-        if (lane == 0) {
-            out[0] = mean + shift;
-            out[1] = fmaxf(m2, 0.f);
+        if (lane == 0 && cnt > 0) {
+            const double mean = p / (double)cnt, m2 = q - p * mean;
+            out[0] = (float)mean;
+            out[1] = (float)(m2 < 0.0 ? 0.0 : m2);  // keeps a NaN
         }
     } else {
         const T* dy = static_cast<const T*>(a.dy);
         const T* gate = static_cast<const T*>(a.gate);
         const float mean = a.mean[(size_t)n * a.G + g], rstd = a.rstd[(size_t)n * a.G + g];
+        float p = 0.f, q = 0.f;
         for (long long i = lane; i < cnt; i += 32 * kBatch) {
             float xv[kBatch], dv[kBatch], zv[kBatch], wv[kBatch], bv[kBatch];
 #pragma unroll

@@ -896,8 +896,10 @@ __global__ void __launch_bounds__(D * 2, D == 64 ? 4 : 2) token_grads_kernel(con
 //     dalpha_log_t = L_{end,0} <G, S> + sum_{r >= t} e_r + sum_{i < t} f_i + sum_{r >= t > i} Z_{r,i}.
 // (The recurrence dalpha_log_t = dalpha_log_{t+1} + q.dq - beta dbeta - ... needs no pairs, but
 // adds and later takes off what each token does to itself, larger by 1 / alpha than what is
-// left: at alpha = e^-8 it lost 1e-3 of the result.)  Four threads a token; decays are running
-// products, sums have a fixed order.  Bound by latency: 264 chunks of d 64 take 50 us.
+// left: at alpha = e^-8 it lost 1e-3 of the result.  A suffix sum of Z's row sums less its column
+// sums does the same with the pairs behind t: one token of e^-8 among slow ones lost 1e-3.)
+// Four threads a token; decays are running products, sums have a fixed order.  Bound by
+// latency: 264 chunks of d 64 take 50 us.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) dalpha_kernel(const Args a)
 {
@@ -1031,9 +1033,21 @@ __global__ void __launch_bounds__(256) dalpha_kernel(const Args a)
         }
     }
     __syncthreads();
-    {   // row sums minus column sums of Z
+    {   // Z summed along each row inside its blocks of 16 columns, in place
+        float* zr = &z[r][16 * part];
         float x = 0.f;
-        for (int c = part; c < kChunk; c += 4) x += z[r][c] - z[c][r];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) zr[c] = x += zr[c];
+    }
+    __syncthreads();
+    {   // the pairs r2 >= r > i that span this thread's token r, and no others: four threads share the rows
+        const int b = r / 16, in = r % 16;
+        float x = 0.f;
+        for (int t = r + part; t < kChunk; t += 4) {
+            float y = in ? z[t][r - 1] : 0.f;
+            for (int c = 0; c < b; ++c) y += z[t][16 * c + 15];
+            x += y;
+        }
         x = sum4(x);
         if (part == 0) rc[r] = x;
     }
@@ -1042,8 +1056,8 @@ __global__ void __launch_bounds__(256) dalpha_kernel(const Args a)
         float y = 0.f;
         for (int w = 0; w < 8; ++w) y += gsum[w];
         for (int t = 0; t < tid; ++t) y += f_[t];
-        float x = 0.f;
-        for (int t = kChunk - 1; t >= tid; --t) x += e_[t] + rc[t];
+        float x = rc[tid];
+        for (int t = kChunk - 1; t >= tid; --t) x += e_[t];
         // nothing enters a sequence's first token from no state: its decay has no effect
         a.dalpha_log[(size_t)(cr.row0 + tid) * a.H + h] = tid == 0 && cr.first && !a.S0 ? 0.f : x + y;
     }

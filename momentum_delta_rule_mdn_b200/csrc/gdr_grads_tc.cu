@@ -11,9 +11,13 @@
 // Z_{r,i} = M1_{r,i} q_r.k_i - M2_{r,i} k_r.k_i for i < r,
 //     dalpha_log_t = aC <G, S> + sum_{r >= t} (scale D_r (S^T q_r) . do_r - XS_r . dv_r)
 //                  + sum_{i < t} gam_i (G^T k_i) . vtilde_i + sum_{r >= t > i} Z_{r,i}.
-// The last is a suffix sum of (row sum - column sum) of Z.  (The shorter recurrence
+// Every term of it carries the decay of token t.  The pairs are added up by blocks of 16 x 16:
+// whole blocks behind and before t's, columns before t of the blocks behind, rows from t on of
+// the blocks before, and t's rectangle of its diagonal block.  (The shorter recurrence
 // dalpha_log_t = dalpha_log_{t+1} + q.dq - beta dbeta - ... adds and later takes off what
-// each token does to itself: with alpha = e^-3 it lost 1.5e-4 of the result.)
+// each token does to itself: with alpha = e^-3 it lost 1.5e-4 of the result.  A suffix sum of
+// Z's row sums less its column sums does so with the pairs behind t: a token of e^-8 among slow
+// ones was 1e-3 off.)
 //
 // dq and dk are rounded to bf16, so S, G, M1, M2 and the scaled rows enter as single
 // bf16 terms.  The gate gradients are fp32: their products P1, P2 and [K; Q] K^T have
@@ -46,9 +50,12 @@ constexpr uint32_t M1 = GB + 32768;      // M1, -M2: 64 rows x 128 B
 constexpr uint32_t M2 = M1 + 8192;
 constexpr uint32_t VEC = M2 + 8192;      // gate vectors
 constexpr uint32_t REC = VEC + 1024;     // the chunk's record
-constexpr uint32_t CS = REC + kBwdRecBytes;  // sums of Z by the warps that formed them: [4][128] of rows
-constexpr int kCsCols = 512;             // (lanes 0..63 of M2, 64..127 of M1), [4][64] of columns
-constexpr uint32_t GS = CS + (512 + 256) * 4;  // [4][64] sums of po, px, pb, pw over the slices; [256]: of gs
+// Sums of Z by the warps that formed them, of M2's part and of M1's: [4 column blocks][128] of a
+// block's rows (lanes 0..63 of M2, 64..127 of M1), [4 quads][2][64] of its columns, 16 rows each,
+// [2][64] of the diagonal blocks' rectangles
+constexpr uint32_t CS = REC + kBwdRecBytes;
+constexpr int kCsCols = 512, kCsDiag = 1024;
+constexpr uint32_t GS = CS + (1024 + 128) * 4;  // [4][64] sums of po, px, pb, pw over the slices; [256]: of gs
 constexpr uint32_t BT = GS + 4 * 256 + 16;   // [4] block factors
 constexpr uint32_t BARS = BT + 16;
 constexpr uint32_t MISC = BARS + 48;
@@ -293,22 +300,32 @@ grads_kernel(const __grid_constant__ GradMaps tm, const Args a, const long long 
                     uint8_t* dst = sm + (m1 ? M1 : M2);
                     st_bf16x8(dst + sw128_off(r, 2 * I), p);
                     st_bf16x8(dst + sw128_off(r, 2 * I + 1), p + 8);
-                    // column sums over the warp's 32 rows: halve the columns a lane holds per step
+                    // sums of 16 columns over 16 rows, column lane % 16 in each lane: halve the
+                    // columns a lane holds per step
+                    auto over_rows = [&](float (&v)[16]) {
 #pragma unroll
-                    for (int w = 8; w >= 1; w >>= 1) {
-                        const bool up = lane & w;
+                        for (int w = 8; w >= 1; w >>= 1) {
+                            const bool up = lane & w;
 #pragma unroll
-                        for (int j = 0; j < w; ++j) {
-                            const float other = __shfl_xor_sync(0xffffffffu, up ? g[j] : g[j + w], w);
-                            g[j] = (up ? g[j + w] : g[j]) + other;
+                            for (int j = 0; j < w; ++j) {
+                                const float other = __shfl_xor_sync(0xffffffffu, up ? v[j] : v[j + w], w);
+                                v[j] = (up ? v[j + w] : v[j]) + other;
+                            }
                         }
+                        return v[0];
+                    };
+                    if (diag) {  // of column i, what the rows from i on hold before it
+                        float before = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            p[j] = I == R && j <= (r & 15) ? before : 0.f;
+                            before += g[j];
+                        }
+                        const float x = over_rows(p);
+                        if (I == R) cs[kCsDiag + (m1 ? 64 : 0) + r] = x;
                     }
-                    g[0] += __shfl_xor_sync(0xffffffffu, g[0], 16);
-                    if (lane < 16) cs[kCsCols + 64 * quad + 16 * I + lane] = g[0];
+                    cs[kCsCols + 128 * quad + (lane >> 4) * 64 + 16 * I + (lane & 15)] = over_rows(g);
                     rows[I * 128 + quad * 32 + lane] = sum;
-                } else {  // no columns right of the warp's rows
-                    if (lane < 16) cs[kCsCols + 64 * quad + 16 * I + lane] = 0.f;
-                    rows[I * 128 + quad * 32 + lane] = 0.f;
                 }
                 tc_fence_before_sync();
             }
@@ -360,42 +377,70 @@ grads_kernel(const __grid_constant__ GradMaps tm, const Args a, const long long 
                 }
                 mma_commit_elect(&bars[4]);
             } else if (warp == 1) {
-                // ---- the head's gate gradients
-                float c[2], b[2], w_[2];
+                // ---- the head's gate gradients: every sum over the terms that count, none taken off
+                float c[2], b[2], w_[2], x[3][2], col[2] = {0.f, 0.f};
                 const float end = gs[256];
+                const int blk = lane >> 3;  // of this lane's two tokens
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int r = 2 * lane + e;
-                    float rs = 0.f, col = 0.f;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        rs += rows[k * 128 + r] + rows[k * 128 + 64 + r];
-                        col += cs[kCsCols + 64 * k + r];
+                    for (int k = 0; k < 3; ++k) {
+                        x[k][e] = k < blk ? rows[k * 128 + r] + rows[k * 128 + 64 + r] : 0.f;
+                        const int R = k + 1;
+                        const float* y = cs + kCsCols + (R >> 1) * 128 + (R & 1) * 64 + r;
+                        if (R > blk) col[e] += y[0] + y[256];
                     }
-                    c[e] = (gs[r] - gs[64 + r]) + (rs - col);
+                    c[e] = gs[r] - gs[64 + r];
                     b[e] = gs[128 + r];
                     w_[e] = gs[192 + r];
                     if (r >= cr.valid) c[e] = w_[e] = 0.f;
                 }
-                float pre = w_[0] + w_[1];  // inclusive prefix sum over lanes
+                float pre = w_[0] + w_[1];  // sums over the lanes up to this one
+                float s = c[0] + c[1];      // ... from this one on
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const float y = __shfl_up_sync(0xffffffffu, pre, o);
+                    const float z = __shfl_down_sync(0xffffffffu, s, o);
                     if (lane >= o) pre += y;
+                    if (lane + o < 32) s += z;
                 }
-                pre -= w_[0] + w_[1];       // of the tokens before this lane's
-                float s = c[0] + c[1];  // inclusive suffix sum over lanes
+                pre = __shfl_up_sync(0xffffffffu, pre, 1);  // of the lanes before, of the lanes behind
+                s = __shfl_down_sync(0xffffffffu, s, 1);
+                if (lane == 0) pre = 0.f;
+                if (lane == 31) s = 0.f;
+                // the same inside the block: columns before the token, rows from it on
+                float cpre = col[0] + col[1], row[2], rsuf;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const float y = __shfl_down_sync(0xffffffffu, s, o);
-                    if (lane + o < 32) s += y;
+                for (int e = 0; e < 2; ++e) row[e] = x[0][e] + x[1][e] + x[2][e];
+                rsuf = row[0] + row[1];
+                float b0 = x[0][0] + x[0][1], b1 = x[1][0] + x[1][1];  // whole blocks, of columns 0 .. 15, 16 .. 31
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) {
+                    const float y = __shfl_up_sync(0xffffffffu, cpre, o, 8);
+                    const float z = __shfl_down_sync(0xffffffffu, rsuf, o, 8);
+                    if ((lane & 7) >= o) cpre += y;
+                    if ((lane & 7) + o < 8) rsuf += z;
+                    b0 += __shfl_xor_sync(0xffffffffu, b0, o);
+                    b1 += __shfl_xor_sync(0xffffffffu, b1, o);
                 }
+                cpre = __shfl_up_sync(0xffffffffu, cpre, 1, 8);
+                rsuf = __shfl_down_sync(0xffffffffu, rsuf, 1, 8);
+                if ((lane & 7) == 0) cpre = 0.f;
+                if ((lane & 7) == 7) rsuf = 0.f;
+                const float b20 = __shfl_sync(0xffffffffu, b0, 16), b30 = __shfl_sync(0xffffffffu, b0, 24);
+                const float b31 = __shfl_sync(0xffffffffu, b1, 24);
+                const float whole = blk == 1 ? b20 + b30 : blk == 2 ? b30 + b31 : 0.f;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int r = 2 * lane + e;
                     if (r < cr.valid) {
                         const size_t at = (size_t)(cr.row0 + r) * a.H + h;
-                        float y = (e == 0 ? s : s - c[0]) + (e == 0 ? pre : pre + w_[0]) + end;
+                        const float pairs = cs[kCsDiag + r] + cs[kCsDiag + 64 + r] + whole +
+                                            (e == 0 ? cpre : cpre + col[0]) +
+                                            (e == 0 ? row[0] + (row[1] + rsuf) : row[1] + rsuf);
+                        float y = (e == 0 ? c[0] + (c[1] + s) : c[1] + s) + (e == 0 ? pre : pre + w_[0]) + end +
+                                  pairs;
                         // nothing enters a sequence's first token from no state: its decay has no effect
                         if (r == 0 && cr.first && !a.S0) y = 0.f;
                         a.dalpha_log[at] = y;

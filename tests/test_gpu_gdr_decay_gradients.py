@@ -5,8 +5,9 @@ With S the state before token t and G' the adjoint it is paired with, dalpha_log
 alpha_t <G', S>, an inner product of d x d matrices, of size alpha_t |G'| |S| / d where they are
 not related.  Tolerances, of that size: fp32, some ten sums of d products, each off by some
 sqrt(d) roundings of 2^-24 / sqrt(3): 1.3e-6 in the mean square, three times that at the worst
-of some hundred tokens, and a factor of two: 1e-5.  Where alpha is 0 in fp32 every term is, and
-the result."""
+of some hundred tokens, and a factor of two: 1e-5.  Tensor cores: seven factors on the way
+are two bf16 terms, 2^-17 / sqrt(3) each in the mean square, 1.2e-5, three times that: 4e-5.
+Where alpha is 0 in fp32 every term is, and the result."""
 import pytest
 import torch
 
@@ -38,7 +39,7 @@ def sizes(q, k, alpha_log, beta, scale, vt, do, S0, dS_T):
 
 
 @pytest.mark.parametrize("off", [(0, 200), (0, 33, 33, 170, 200)])
-@pytest.mark.parametrize("dtype,d,flags", [(F32, 64, 0), (F32, 128, 0), (BF16, 64, 0),
+@pytest.mark.parametrize("dtype,d,flags", [(F32, 64, 0), (F32, 128, 0), (BF16, 64, 0), (BF16, 128, 0),
                                            (BF16, 128, E.MDN_FORCE_SIMT)])
 @pytest.mark.parametrize("H,Hk", [(2, 2), (4, 2), (24, 24)])
 def test_single_tokens_of_strong_decay(H, Hk, dtype, d, flags, off):
@@ -62,7 +63,7 @@ def test_single_tokens_of_strong_decay(H, Hk, dtype, d, flags, off):
         got = mdn.gdr_chunk_bwd_varlen(q, k, al, be, cu, None, vt, do, S0.cuda(), dST.cuda(),
                                        flags=flags)["dalpha_log"]
     got, vt = got.cpu().to(R.F64), vt.cpu()
-    tol = 1e-5
+    tol = 4e-5 if (dtype, d, flags) == (BF16, 128, 0) else 1e-5
     for s in range(N):
         sl = slice(off[s], off[s + 1])
         ref, size = sizes(*(one[n][sl] for n in ("q", "k", "alpha_log", "beta")), d ** -0.5, vt[sl],

@@ -592,6 +592,7 @@ mdn_status mdn_gdr_step(const void *q, const void *k, const void *v, mdn_dtype i
  *   weight, bias  [C] fp32, both or neither (NULL: 1 and 0).
  *   eps         >= 0.  var is the mean squared distance from the mean.
  *   mean, rstd  [N,G] fp32 outputs (the backward pass reads them).
+ *               With no rows (L = 0) nothing is written.
  *   workspace   at least mdn_group_norm_workspace_size(..., 0) bytes, 16-byte
  *               aligned; NULL where that is 0 (L = 1 and up to 256 channels a
  *               group at any alignment).

@@ -12,6 +12,7 @@ over the L x C/groups values of a group.  The output of a token mixer,
 from __future__ import annotations
 
 import functools
+import math
 from typing import Optional
 
 import torch
@@ -56,7 +57,8 @@ def group_norm_fwd(x, groups: int, weight=None, bias=None, gate=None, eps: float
                    act: str = "silu", *, out=None, workspace: Optional[torch.Tensor] = None,
                    stream: Optional[torch.cuda.Stream] = None):
     """Returns (y, mean, rstd): y of x's shape and type, mean and rstd [N, groups]
-    float32 (what :func:`group_norm_bwd` needs).  ``out`` may hold them preallocated."""
+    float32 (what :func:`group_norm_bwd` needs).  ``out`` may hold them preallocated.
+    Groups of no rows (L = 0) have mean 0 and rstd eps ** -0.5, those of no spread."""
     N, L, C, code = _common(x, groups, weight, bias, gate, act)
     with _On(x.device, stream) as s:
         if out is None:
@@ -71,7 +73,10 @@ def group_norm_fwd(x, groups: int, weight=None, bias=None, gate=None, eps: float
         status = library().mdn_group_norm_fwd(
             _ptr(x), _ptr(gate), code, _ptr(weight), _ptr(bias), N, L, C, groups, float(eps),
             _ACT[act], _ptr(y), _ptr(mean), _ptr(rstd), ws, ws_bytes, s)
-    _check(status, "mdn_group_norm_fwd")
+        _check(status, "mdn_group_norm_fwd")
+        if L == 0:  # the library has no rows to take statistics of and writes none
+            mean.zero_()
+            rstd.fill_(float(eps) ** -0.5 if eps > 0 else math.inf)
     return y, mean, rstd
 
 

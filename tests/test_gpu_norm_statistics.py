@@ -64,3 +64,21 @@ def test_far_values_anywhere(shape):
     at = torch.randint(0, x.numel(), (max(4, x.numel() // 20000),), generator=g, device="cuda")
     x.view(-1)[at] = 2000 * torch.randn(at.numel(), generator=g, device="cuda")
     check(x, G)
+
+
+@pytest.mark.parametrize("eps", [1e-5, 0.25, 0.0])
+@pytest.mark.parametrize("given", [False, True])
+def test_no_rows(given, eps):
+    """Groups of no rows: mean 0 and rstd 1 / sqrt(eps), whatever the memory held."""
+    x = torch.empty(3, 0, 64, device="cuda")
+    held = torch.full((3, 4), 7.0, device="cuda"), torch.full((3, 4), 7.0, device="cuda")
+    out = (torch.empty_like(x), *held) if given else None
+    del held
+    y, mean, rstd = mdn.group_norm_fwd(x, 4, eps=eps, out=out)
+    assert y.shape == x.shape and mean.shape == rstd.shape == (3, 4)
+    assert (mean == 0).all()
+    want = torch.tensor(eps, dtype=torch.float64).rsqrt().float().expand(3, 4)
+    assert torch.allclose(rstd.cpu(), want, rtol=2.0 ** -22, atol=0)   # eps and the result in fp32
+    w = torch.ones(64, device="cuda")
+    g = mdn.group_norm_bwd(x, 4, mean, rstd, x, w, w)
+    assert g["dx"].shape == x.shape and (g["dweight"] == 0).all() and (g["dbias"] == 0).all()

@@ -59,6 +59,11 @@ def _need(t, like, dtype, shape, name):
                          f"{t.dtype} {tuple(t.shape)} contiguous={t.is_contiguous()} on {t.device}")
 
 
+def _fits(*sizes) -> bool:
+    """Whether sizes fit the library's ints (a conversion would keep the low 32 bits)."""
+    return all(0 <= n < 1 << 31 for n in sizes)
+
+
 def _heads(q, ref, ref_name, lead):
     """(rows..., Hk, H, d) of a call, its tensors' shapes checked against each other."""
     if q.dim() != lead + 2 or ref.dim() != lead + 2:
@@ -101,6 +106,8 @@ def gdr_chunk_workspace_size(B: int, T: int, Hk: int, H: int, d: int, C: int = 6
                              dtype: torch.dtype = torch.bfloat16, flags: int = 0, *,
                              packed: bool = False, backward: bool = False) -> int:
     """Scratch bytes of the chunk calls (packed: B sequences in T tokens); 0 if unsupported."""
+    if not _fits(B, T, Hk, H, d, C):
+        return 0
     return _chunk_bytes(B, T, Hk, H, d, C, dtype, int(flags), packed, backward)
 
 

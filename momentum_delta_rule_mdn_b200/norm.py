@@ -19,7 +19,7 @@ import torch
 
 from . import _lib
 from .api import _check, _dtype_code, _ptr, library
-from .gdr import _need, _On, _workspace
+from .gdr import _fits, _need, _On, _workspace
 
 _ACT = {"none": _lib.MDN_ACT_NONE, "silu": _lib.MDN_ACT_SILU}
 
@@ -32,6 +32,8 @@ def _common(x, groups, weight, bias, gate, act):
     N, L, C = x.shape
     if groups < 1 or C == 0 or C % groups:
         raise ValueError(f"{C} channels do not divide into {groups} groups")
+    if max(N, L, C) >= 1 << 31:  # the library's ints would keep the low 32 bits
+        raise ValueError(f"x: sizes must be below 2^31, got {tuple(x.shape)}")
     if (weight is None) != (bias is None):
         raise ValueError("weight and bias: give both or neither")
     code = _dtype_code(x)
@@ -45,6 +47,8 @@ def _common(x, groups, weight, bias, gate, act):
 def group_norm_workspace_size(N: int, L: int, C: int, groups: int,
                               dtype: torch.dtype = torch.bfloat16, backward: bool = False) -> int:
     """Scratch bytes of :func:`group_norm_fwd` or :func:`group_norm_bwd`."""
+    if not _fits(N, L, C, groups):
+        return 0
     return _bytes(N, L, C, groups, _lib.MDN_BF16 if dtype == torch.bfloat16 else _lib.MDN_F32, backward)
 
 

@@ -548,7 +548,8 @@ cudaError_t launch_chain(const Args& a, bool overlap, cudaStream_t s)
 // partial wave runs meanwhile.  With r chain steps per operand chunk (11k cycles at three
 // CTAs an SM), L minimises  L r + max(NT, rest / U r + 1).  Measured, operands and chain:
 // 16384 tokens of 16 heads 350 -> 308 us, packed sequences of 1 to 24576 tokens 792 -> 683,
-// 4 x 2048 tokens of 8 heads 84 -> 77, 8 x 4096 of 16 (256 CTAs) 416 -> 393.  Whole waves
+// 4 x 2048 tokens of 8 heads 84 -> 77, 8 x 4096 of 16 (256 CTAs) 416 -> 393 (in a loop of
+// seconds, at the power cap, 411 to 415).  Whole waves
 // only: nothing is reserved and nothing overlaps.
 cudaError_t launch_fwd_tc(const Args& a, cudaStream_t s)
 {

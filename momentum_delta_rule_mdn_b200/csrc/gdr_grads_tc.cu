@@ -27,7 +27,7 @@
 // phases: [K; Q] K^T and the P products, the rows of M (twelve warps, a 32 x 16 block
 // each) and the scaling of dO, Vtilde and dv in place, the products, the stores; the next
 // chunk's loads run under the last.  A scheduler with one warp issues every fifth cycle at
-// best, so the phases' work is spread over 16 warps.  32 heads of 2048 tokens: 62 us (one
+// best, so the phases' work is spread over 16 warps.  32 heads of 2048 tokens: 65 us (one
 // CTA a chunk took 73, on 8 warps 113).
 #include "gdr_tc.cuh"
 
@@ -275,7 +275,7 @@ grads_kernel(const __grid_constant__ GradMaps tm, const Args a, const long long 
                     for (int y = 0; y < 4; ++y) {
                         const float4 s4 = gv.get4(kSbeta, 4 * I + y);
                         float f[4] = {off * s4.x, off * s4.y, off * s4.z, off * s4.w};
-                        if (diag) {  // the warp's rows include this block's diagonal
+                        if (diag) {  // the warp's rows include this block's diagonal (__expf: 1e-6 at e^-16)
                             const float4 p4 = gv.get4(kP, 4 * I + y), l4 = gv.get4(kPlo, 4 * I + y);
                             const float4 b4 = gv.get4(kBeta, 4 * I + y);
                             const float pv[4] = {p4.x, p4.y, p4.z, p4.w}, lv[4] = {l4.x, l4.y, l4.z, l4.w};

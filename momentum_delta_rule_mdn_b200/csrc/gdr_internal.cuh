@@ -135,10 +135,10 @@ inline long long rows(const Args& a) { return a.cu_s ? a.T : (long long)a.B * a.
 inline long long chains(const Args& a) { return (long long)a.B * a.H; }
 inline long long chunks(const Args& a) { return a.cu_s ? a.NT : (long long)a.B * a.NT; }
 
-// CUDA-core kernels, fp32 arithmetic, any supported type and d.
-// Tensor-core path (bf16).
+// Tensor-core path (bf16; backward d = 128).
 cudaError_t launch_fwd_tc(const Args& a, cudaStream_t s);
 cudaError_t launch_bwd_tc(const Args& a, cudaStream_t s);
+// CUDA-core kernels, fp32 arithmetic, any supported type and d.
 cudaError_t launch_fwd_simt(const Args& a, mdn_dtype dt, cudaStream_t s);
 cudaError_t launch_bwd_simt(const Args& a, mdn_dtype dt, cudaStream_t s);
 // Sums of dqp, dkp over the value heads of each key head, in head order.

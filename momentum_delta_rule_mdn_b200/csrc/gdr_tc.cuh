@@ -123,7 +123,7 @@ __device__ __forceinline__ void mma_commit_elect(uint64_t* bar)
         : "memory");
 }
 
-// a + b exactly, as a float and its rounding error
+// x + y exactly, as a float and its rounding error (Knuth's two-sum)
 __device__ __forceinline__ float two_sum(float x, float y, float& err)
 {
     const float s = __fadd_rn(x, y), z = __fsub_rn(s, x);
